@@ -53,10 +53,14 @@ enum moe_status_code {
 
 enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 };
 
+/* Type of the activations that moe_expert_ffn_w4 reads: a moe_dtype, or e4m3 with scales. */
+enum moe_act_dtype { MOE_E4M3 = 2 };
+
 /* Bits of the device status word (sticky until moe_status_reset). */
 enum moe_device_status {
   MOE_STATUS_BAD_INDEX = 1, /* an expert id, token id or slot was out of range; element skipped */
-  MOE_STATUS_TIMEOUT = 2    /* a bounded on-device wait gave up; results are invalid */
+  MOE_STATUS_TIMEOUT = 2,   /* a bounded on-device wait gave up; results are invalid */
+  MOE_STATUS_NOT_FINITE = 4 /* moe_adamw_step met a gradient that is not finite; elements skipped */
 };
 
 /* moe_route flags */
@@ -78,7 +82,12 @@ enum moe_op {
   MOE_OP_COMBINE = 7,
   MOE_OP_COMBINE_BWD = 8,
   MOE_OP_ALL = 9, /* the largest of the above: one workspace for the whole layer */
-  MOE_OP_GSHARD = 10 /* the capacity-buffer comparison path (moe_gshard_*) */
+  MOE_OP_GSHARD = 10, /* the capacity-buffer comparison path (moe_gshard_*) */
+  /* the operators around the layer (not part of MOE_OP_ALL) */
+  MOE_OP_ADD_RMSNORM = 11,
+  MOE_OP_ADD_RMSNORM_BWD = 12,
+  MOE_OP_ADAMW = 13,
+  MOE_OP_EXPERT_FFN_W4 = 14
 };
 
 /* Workspace bytes `op` needs at these sizes (always >= 256, a multiple of 256). */
@@ -354,6 +363,93 @@ int moe_gshard_dispatch(const void* x, const void* dispatch_mask, int T, int E, 
  */
 int moe_gshard_combine(const float* combine_w, const void* ye, int T, int E, int C, int h, int dtype, void* y,
                        void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The operators around the layer: the norm in front of it, the optimizer step on its parameters, and
+ * its experts over 4-bit weights for decode steps.
+ *
+ * moe_add_rmsnorm -- the residual's addition and the root-mean-square norm in one pass:
+ *   s = round(x + residual);  rstd[t] = 1 / sqrt(mean_c(s[t,c]^2) + eps);
+ *   v = s * rstd * gamma (fp32);  y = round(v);
+ *   q = e4m3(v / q_scale), round to nearest even, values beyond +-448 * q_scale saturate;
+ *   q_scale[t,g] = max(amax of v over columns 128 g .. 128 g + 127, 2^-100) / 448.
+ * The norm is of the stored (rounded) s, which is what the backward reads.  A NaN stays a NaN in s, y
+ * and q, and leaves q_scale to the group's other columns.
+ * x, residual, s, y: [T,h] dtype.  residual NULL: s is x itself, and the argument s must be NULL.
+ * gamma: [h] fp32.  y may be NULL when q is given; q ([T,h] bytes) and q_scale ([T,ceil(h/128)] fp32)
+ * are both given or both NULL.  rstd: [T] fp32 or NULL.  s may be x or residual itself.
+ * Requires h % 8 == 0 and h <= 16384.  Workspace: the status header (nothing is flagged).
+ */
+int moe_add_rmsnorm(const void* x, const void* residual, const float* gamma, float eps, int T, int h, int dtype,
+                    void* s, void* y, void* q, float* q_scale, float* rstd, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/*
+ * Its adjoint, from the saved s and rstd.  With g = dy * gamma and xh = s * rstd:
+ *   ds = round(ds_add + rstd * (g - xh * mean_c(g * xh)));  dgamma[c] = sum_t dy[t,c] * xh[t,c].
+ * ds is the gradient of x and of residual.  dy, s, ds: [T,h] dtype; ds_add: [T,h] dtype (the gradient
+ * that reaches s along the residual stream) or NULL; dgamma: [h] fp32 (overwritten; zeros for T = 0).
+ * ds may be ds_add itself.  Deterministic: dgamma sums partial rows in the workspace in a fixed order.
+ */
+int moe_add_rmsnorm_bwd(const void* dy, const void* s, const float* gamma, const float* rstd, const void* ds_add,
+                        int T, int h, int dtype, void* ds, float* dgamma, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One AdamW step over `n` tensors (any number; one launch per 384).  With t = *step:
+ *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
+ *   p -= lr * (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)), fp32.
+ * The arrays params .. numels, weight_decays and dtypes are HOST arrays of n entries, read during the
+ * call; what they point to is on the device.  dtypes[i] MOE_F32: params[i] and grads[i] are fp32 and
+ * masters[i] is ignored.  MOE_BF16: both are bf16, p is masters[i] (fp32), and params[i] receives its
+ * rounding.  masters may be NULL when no tensor is bf16.  numels[i] may be 0 (its pointers are not
+ * looked at).
+ * state_bits 32: ms[i] and vs[i] are fp32; m_scales and v_scales are NULL.  state_bits 8: ms[i] holds
+ * e4m3 and vs[i] e5m2 codes, with an fp32 scale per 256 elements in m_scales[i] and v_scales[i]
+ * (ceil(numel/256) entries): m = code * scale, scale = max(amax|m|, 2^-100) / 2^8, and v likewise with
+ * 2^15.  p is updated from the unrounded states; then each state is rounded up or down at random, with
+ * the probability of what is cut off (so their moving averages are unbiased), and a positive v never
+ * to zero.  The 16 random bits of m and of v (low and high half) are word e % 4 of Philox4x32-7 with
+ * key `seed` and counter (e / 4 low, e / 4 high, tensor number, step) for element e of a tensor: equal
+ * seeds and steps give equal states.  All-zero codes and scales are the state before the first step.
+ * lr: fp32[1], step: int32[1] (>= 1, the number of this step), grad_scale: fp32[1] or NULL (1), on the
+ * device, so that a captured step follows them.  step < 1 sets MOE_STATUS_BAD_INDEX and changes nothing.
+ * An element whose g^2 is not finite keeps p, m and v (in 8 bits as they stand for; a new block scale
+ * may round them again) and sets MOE_STATUS_NOT_FINITE.  0 <= beta1, beta2 < 1; eps > 0.
+ */
+int moe_adamw_step(int n, void* const* params, const void* const* grads, float* const* masters, void* const* ms,
+                   void* const* vs, float* const* m_scales, float* const* v_scales, const int64_t* numels,
+                   const float* weight_decays, const int32_t* dtypes, int state_bits, const float* lr,
+                   const int32_t* step, const float* grad_scale, double beta1, double beta2, double eps,
+                   uint64_t seed, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 4-bit expert weights.  W: [E,K,N] dtype (K inputs: h for W1 and W3, f for W2).  q: [E,N,K/2] bytes:
+ * input 2i of an output in the low half of byte i, 2i+1 in the high half, each offset by 8.  scale:
+ * [E,N,ceil(K/group)] bf16, one for `group` consecutive inputs of an output:
+ *   scale = bf16(amax / 7);  nibble = clamp(rint(w / scale), -8, 7) + 8;  w ~ (nibble - 8) * scale.
+ * group: 32, 64 or 128.  Requires K % 32 == 0 and N % 32 == 0; the last group of a row may be short.
+ * A weight that is not a number becomes 0; an infinite one makes its group's scale infinite.
+ */
+int moe_quantize_w4(const void* W, int E, int K, int N, int dtype, int group, void* q, void* scale, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/*
+ * The routed experts over 4-bit weights, for decode steps (few tokens): dispatch, experts and combine
+ * of the layer in one call, straight from the gate's selection (no PFT build):
+ *   a = silu(W1_e x[t]) * (W3_e x[t]);  y[t] = sum_j topk_w[t,j] * W2_e a, e = topk_idx[t,j], j ascending.
+ * x: [T,h] in x_dtype: the call's dtype, or MOE_E4M3 (dtype MOE_BF16 then) with x_scale [T,ceil(h/128)]
+ * fp32, as moe_add_rmsnorm writes them; x_scale is NULL otherwise.  topk_idx: [T,k] int32, topk_w:
+ * [T,k] fp32 (these three at any address of their type: rows of a larger batch may be passed as they are).  W1q, W3q: [E,f,h/2], W1s, W3s: [E,f,ceil(h/group)]; W2q: [E,h,f/2], W2s:
+ * [E,h,ceil(f/group)].  y: [T,h] dtype.  Sums are fp32 over the exact 4-bit values (a group's sum is
+ * scaled once); a is rounded to dtype.  An id outside [0,E) sets MOE_STATUS_BAD_INDEX and adds nothing.
+ * An expert's weights are read once for every 8 of its rows: above some 32 rows an expert, moe_expert_ffn
+ * over unpacked weights is the faster call.  Requires h % 32 == 0, f % 32 == 0, 1 <= k <= E <= 1024 and
+ * T*k <= 65536.
+ */
+int moe_expert_ffn_w4(const void* x, const float* x_scale, const int32_t* topk_idx, const float* topk_w,
+                      const void* W1q, const void* W1s, const void* W3q, const void* W3s, const void* W2q,
+                      const void* W2s, int T, int k, int E, int h, int f, int group, int x_dtype, int dtype, void* y,
+                      void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,14 +18,15 @@ LIB_PATH = os.path.join(HERE, "libmoe_pft.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE = (
     0, -1, -2, -3, -4, -5)
-MOE_F32, MOE_BF16 = 0, 1
-MOE_STATUS_BAD_INDEX, MOE_STATUS_TIMEOUT = 1, 2
+MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
+MOE_STATUS_BAD_INDEX, MOE_STATUS_TIMEOUT, MOE_STATUS_NOT_FINITE = 1, 2, 4
 MOE_ROUTE_FROM_LOGITS, MOE_ROUTE_SIGMOID, MOE_ROUTE_RENORM = 1, 2, 4
 (MOE_OP_ROUTE, MOE_OP_ROUTE_BWD, MOE_OP_PFT_BUILD, MOE_OP_DISPATCH, MOE_OP_DISPATCH_BWD,
- MOE_OP_EXPERT_FFN, MOE_OP_EXPERT_FFN_BWD, MOE_OP_COMBINE, MOE_OP_COMBINE_BWD, MOE_OP_ALL, MOE_OP_GSHARD) = range(11)
+ MOE_OP_EXPERT_FFN, MOE_OP_EXPERT_FFN_BWD, MOE_OP_COMBINE, MOE_OP_COMBINE_BWD, MOE_OP_ALL, MOE_OP_GSHARD,
+ MOE_OP_ADD_RMSNORM, MOE_OP_ADD_RMSNORM_BWD, MOE_OP_ADAMW, MOE_OP_EXPERT_FFN_W4) = range(15)
 
 # C signatures: (name, restype, argtypes).  P = pointer, I = int, Z = size_t.
-_P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _Z, _D = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
 SIGNATURES = {
     "moe_abi_version": (_I, []),
     "moe_kernel_launches": (ctypes.c_uint64, []),
@@ -57,6 +58,12 @@ SIGNATURES = {
     "moe_gshard_dispatch": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _Z, _P]),
     "moe_gshard_combine": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _Z, _P]),
     "moe_combine_bwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
+    "moe_add_rmsnorm": (_I, [_P, _P, _P, ctypes.c_float, _I, _I, _I, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "moe_add_rmsnorm_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P]),
+    "moe_adamw_step": (_I, [_I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _D, _D, _D, ctypes.c_uint64,
+                            _P, _Z, _P]),
+    "moe_quantize_w4": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
+    "moe_expert_ffn_w4": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _Z, _P]),
 }
 
 
@@ -311,3 +318,98 @@ def moe_gshard_combine(combine_w, ye, y, ws):
     h = ye.shape[2]
     _call("moe_gshard_combine", _p(combine_w), _p(ye), T, E, C, h, _dtype_code(ye), _p(y), _p(ws), ws.numel(),
           _stream())
+
+
+def _check(t, name, dtype, shape):
+    """Refuse a tensor whose type or shape the call would misread (None passes); returns its pointer."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    return _p(t)
+
+
+def moe_add_rmsnorm(x, residual, gamma, eps, s, y, q, q_scale, rstd, ws):
+    """s = x + residual (both None: s is x) and its RMSNorm: y in x's dtype and/or q (float8_e4m3fn) with
+    q_scale [T, ceil(h/128)] fp32; rstd [T] fp32 (or None) is what the backward needs."""
+    shape, dt = tuple(x.shape), x.dtype
+    T, h = shape
+    _call("moe_add_rmsnorm", _p(x), _check(residual, "residual", dt, shape), _check(gamma, "gamma", torch.float32, (h,)),
+          eps, T, h, _dtype_code(x), _check(s, "s", dt, shape), _check(y, "y", dt, shape),
+          _check(q, "q", torch.float8_e4m3fn, shape), _check(q_scale, "q_scale", torch.float32, (T, (h + 127) // 128)),
+          _check(rstd, "rstd", torch.float32, (T,)), _p(ws), ws.numel(), _stream())
+
+
+def moe_add_rmsnorm_bwd(dy, s, gamma, rstd, ds_add, ds, dgamma, ws):
+    """ds = ds_add (or 0) + the norm's gradient for dy; dgamma [h] fp32."""
+    shape, dt = tuple(s.shape), s.dtype
+    T, h = shape
+    _call("moe_add_rmsnorm_bwd", _check(dy, "dy", dt, shape), _p(s), _check(gamma, "gamma", torch.float32, (h,)),
+          _check(rstd, "rstd", torch.float32, (T,)), _check(ds_add, "ds_add", dt, shape), T, h, _dtype_code(s),
+          _check(ds, "ds", dt, shape), _check(dgamma, "dgamma", torch.float32, (h,)), _p(ws), ws.numel(), _stream())
+
+
+def _pointers(tensors, n, name, dtypes, sizes):
+    """A C array of the n tensors' device pointers; dtypes and sizes are what each must have."""
+    if len(tensors) != n:
+        raise ValueError(f"{name}: {len(tensors)} tensors for {n} parameters")
+    a = (ctypes.c_void_p * n)()
+    for i, t in enumerate(tensors):
+        if t is None:
+            continue
+        if t.dtype != dtypes[i] or t.numel() != sizes[i] or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {sizes[i]} {dtypes[i]}, got "
+                             f"{t.numel()} {t.dtype}")
+        a[i] = t.data_ptr()
+    return a
+
+
+def moe_adamw_step(params, grads, masters, m, v, m_scale, v_scale, weight_decay, lr, step, grad_scale, beta1, beta2,
+                   eps, seed, ws):
+    """One AdamW step over lists of tensors, in place.  bf16 parameters have an fp32 master (None for fp32 ones;
+    ``masters`` may be None when there are none).  States: fp32, or with ``m_scale`` and ``v_scale`` (lists of fp32, one
+    value per 256 elements) float8_e4m3fn m and float8_e5m2 v.  ``weight_decay``: a number, or one per tensor.  ``lr``
+    (fp32[1]), ``step`` (int32[1], this step's number) and ``grad_scale`` (fp32[1] or None) are on the device."""
+    n = len(params)
+    dts = [t.dtype for t in params]
+    sizes = [t.numel() for t in params]
+    codes = (ctypes.c_int32 * n)(*[_dtype_code(t) for t in params])
+    f32 = [torch.float32] * n
+    q8 = m_scale is not None
+    blocks = [(s + 255) // 256 for s in sizes] if q8 else None
+    if (v_scale is not None) != q8:
+        raise ValueError("m_scale and v_scale go together")
+    wd = (ctypes.c_float * n)(*(weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n))
+    _call("moe_adamw_step", n, _pointers(params, n, "params", dts, sizes), _pointers(grads, n, "grads", dts, sizes),
+          _pointers(masters, n, "masters", f32, sizes) if masters is not None else None,
+          _pointers(m, n, "m", [torch.float8_e4m3fn] * n if q8 else f32, sizes),
+          _pointers(v, n, "v", [torch.float8_e5m2] * n if q8 else f32, sizes),
+          _pointers(m_scale, n, "m_scale", f32, blocks) if q8 else None,
+          _pointers(v_scale, n, "v_scale", f32, blocks) if q8 else None,
+          (ctypes.c_int64 * n)(*sizes), wd, codes, 8 if q8 else 32, _check(lr, "lr", torch.float32, (1,)),
+          _check(step, "step", torch.int32, (1,)), _check(grad_scale, "grad_scale", torch.float32, (1,)), beta1, beta2, eps,
+          seed, _p(ws), ws.numel(), _stream())
+
+
+def moe_quantize_w4(W, group, q, scale, ws):
+    """W [E, K, N] to 4 bits: q [E, N, K/2] uint8 (two inputs a byte) and scale [E, N, ceil(K/group)] bf16."""
+    E, K, N = W.shape
+    _call("moe_quantize_w4", _p(W), E, K, N, _dtype_code(W), group, _check(q, "q", torch.uint8, (E, N, K // 2)),
+          _check(scale, "scale", torch.bfloat16, (E, N, -(-K // group))), _p(ws), ws.numel(), _stream())
+
+
+def moe_expert_ffn_w4(x, x_scale, topk_idx, topk_w, W1q, W1s, W3q, W3s, W2q, W2s, group, y, ws):
+    """The routed experts of a few tokens over 4-bit weights (moe_quantize_w4 of W1, W3 and W2): y [T, h] from x (y's
+    dtype, or float8_e4m3fn with x_scale [T, ceil(h/128)]) and the gate's topk_idx and topk_w [T, k]."""
+    T, k = topk_idx.shape
+    h = y.shape[1]
+    E, f, _ = W1q.shape
+    dt, u8, bf = y.dtype, torch.uint8, torch.bfloat16
+    q8 = x.dtype == torch.float8_e4m3fn
+    up, down = (E, f, -(-h // group)), (E, h, -(-f // group))
+    _call("moe_expert_ffn_w4", _check(x, "x", x.dtype if q8 else dt, (T, h)),
+          _check(x_scale, "x_scale", torch.float32, (T, -(-h // 128))), _check(topk_idx, "topk_idx", torch.int32, (T, k)),
+          _check(topk_w, "topk_w", torch.float32, (T, k)), _check(W1q, "W1q", u8, (E, f, h // 2)), _check(W1s, "W1s", bf, up),
+          _check(W3q, "W3q", u8, (E, f, h // 2)), _check(W3s, "W3s", bf, up), _check(W2q, "W2q", u8, (E, h, f // 2)),
+          _check(W2s, "W2s", bf, down), T, k, E, h, f, group, MOE_E4M3 if q8 else _dtype_code(y), _dtype_code(y),
+          _check(y, "y", dt, (T, h)), _p(ws), ws.numel(), _stream())

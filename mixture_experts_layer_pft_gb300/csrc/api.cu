@@ -1,5 +1,6 @@
 // The exported C ABI (include/moe_pft.h): host-side argument checks, workspace layout and
 // launches.  Every check happens before any launch; the library allocates nothing.
+#include <math.h>
 #include <stdio.h>
 #include <string.h>
 
@@ -179,6 +180,10 @@ size_t moe_workspace_size(int op, int T, int h, int E, int k, int f, int dtype) 
       return hdr + 2 * round256((size_t)Tk * std::max(f, 0) * esize(dtype));
     case MOE_OP_GSHARD:
       return hdr + round256((size_t)Tk * sizeof(int));
+    case MOE_OP_ADD_RMSNORM_BWD:
+      return hdr + round256((size_t)kNormMaxParts * std::max(h, 0) * sizeof(float));
+    case MOE_OP_EXPERT_FFN_W4:  // a in dtype and the experts' output rows in fp32
+      return hdr + round256((size_t)Tk * std::max(f, 0) * esize(dtype)) + round256((size_t)Tk * std::max(h, 0) * sizeof(float));
     case MOE_OP_ALL: {
       size_t m = 0;
       for (int o = 0; o < MOE_OP_ALL; ++o) m = std::max(m, moe_workspace_size(o, T, h, E, k, f, dtype));
@@ -553,6 +558,134 @@ int moe_gshard_combine(const float* combine_w, const void* ye, int T, int E, int
   REQUIRE_PTR(combine_w); REQUIRE_PTR(ye); REQUIRE_PTR(y);
   launch_gshard_combine(dtype, combine_w, ye, T, E, C, h, y, status_of(ws), (cudaStream_t)stream);
   return check_launch("moe_gshard_combine");
+}
+
+int moe_add_rmsnorm(const void* x, const void* residual, const float* gamma, float eps, int T, int h, int dtype,
+                    void* s, void* y, void* q, float* q_scale, float* rstd, void* ws, size_t ws_bytes,
+                    void* stream) {
+  REQUIRE(T >= 0 && h >= 8 && eps >= 0.f, MOE_ERR_INVALID_ARG, "moe_add_rmsnorm: need T >= 0, h >= 8, eps >= 0");
+  REQUIRE(dtype_ok(dtype), MOE_ERR_INVALID_ARG, "moe_add_rmsnorm: bad dtype");
+  REQUIRE(h % 8 == 0 && h <= kNormMaxWidth, MOE_ERR_UNSUPPORTED,
+          "moe_add_rmsnorm: h must be a multiple of 8 and at most 16384");
+  REQUIRE(ws != nullptr && ws_bytes >= moe_workspace_size(MOE_OP_ADD_RMSNORM, T, h, 1, 1, 0, dtype), MOE_ERR_WORKSPACE,
+          "moe_add_rmsnorm: workspace too small");
+  REQUIRE((residual == nullptr) == (s == nullptr) || T == 0, MOE_ERR_INVALID_ARG,
+          "moe_add_rmsnorm: residual and s go together");
+  REQUIRE((q == nullptr) == (q_scale == nullptr) || T == 0, MOE_ERR_INVALID_ARG,
+          "moe_add_rmsnorm: q and q_scale go together");
+  if (T == 0) return MOE_OK;
+  REQUIRE(y != nullptr || q != nullptr, MOE_ERR_INVALID_ARG, "moe_add_rmsnorm: neither y nor q");
+  REQUIRE_PTR(x); REQUIRE_PTR(gamma);
+  REQUIRE(aligned16(residual) && aligned16(s) && aligned16(y) && aligned16(q) && aligned16(q_scale) && aligned16(rstd),
+          MOE_ERR_INVALID_ARG, "moe_add_rmsnorm: a pointer is not 16-byte aligned");
+  launch_add_rmsnorm(dtype, x, residual, gamma, eps, T, h, s, y, q, q_scale, rstd, (cudaStream_t)stream);
+  return check_launch("moe_add_rmsnorm");
+}
+
+int moe_add_rmsnorm_bwd(const void* dy, const void* s, const float* gamma, const float* rstd, const void* ds_add,
+                        int T, int h, int dtype, void* ds, float* dgamma, void* ws, size_t ws_bytes, void* stream) {
+  const cudaStream_t st = (cudaStream_t)stream;
+  REQUIRE(T >= 0 && h >= 8, MOE_ERR_INVALID_ARG, "moe_add_rmsnorm_bwd: need T >= 0, h >= 8");
+  REQUIRE(dtype_ok(dtype), MOE_ERR_INVALID_ARG, "moe_add_rmsnorm_bwd: bad dtype");
+  REQUIRE(h % 8 == 0 && h <= kNormMaxWidth, MOE_ERR_UNSUPPORTED,
+          "moe_add_rmsnorm_bwd: h must be a multiple of 8 and at most 16384");
+  REQUIRE(ws != nullptr && aligned16(ws) && ws_bytes >= moe_workspace_size(MOE_OP_ADD_RMSNORM_BWD, T, h, 1, 1, 0, dtype),
+          MOE_ERR_WORKSPACE, "moe_add_rmsnorm_bwd: workspace too small");
+  REQUIRE_PTR(dgamma);
+  if (T == 0) {
+    cudaMemsetAsync(dgamma, 0, sizeof(float) * h, st);
+    return check_launch("moe_add_rmsnorm_bwd");
+  }
+  REQUIRE_PTR(dy); REQUIRE_PTR(s); REQUIRE_PTR(gamma); REQUIRE_PTR(rstd); REQUIRE_PTR(ds);
+  REQUIRE(aligned16(ds_add), MOE_ERR_INVALID_ARG, "moe_add_rmsnorm_bwd: ds_add not aligned");
+  launch_add_rmsnorm_bwd(dtype, dy, s, gamma, rstd, ds_add, T, h, ds, dgamma,
+                         reinterpret_cast<float*>(static_cast<char*>(ws) + sizeof(WsHeader)), st);
+  return check_launch("moe_add_rmsnorm_bwd");
+}
+
+int moe_adamw_step(int n, void* const* params, const void* const* grads, float* const* masters, void* const* ms,
+                   void* const* vs, float* const* m_scales, float* const* v_scales, const int64_t* numels,
+                   const float* weight_decays, const int32_t* dtypes, int state_bits, const float* lr,
+                   const int32_t* step, const float* grad_scale, double beta1, double beta2, double eps,
+                   uint64_t seed, void* ws, size_t ws_bytes, void* stream) {
+  REQUIRE(n >= 0, MOE_ERR_INVALID_ARG, "moe_adamw_step: need n >= 0");
+  REQUIRE(state_bits == 32 || state_bits == 8, MOE_ERR_INVALID_ARG, "moe_adamw_step: state_bits is 8 or 32");
+  REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 && eps > 0.0, MOE_ERR_INVALID_ARG,
+          "moe_adamw_step: need 0 <= beta1, beta2 < 1 and eps > 0");
+  REQUIRE(ws != nullptr && ws_bytes >= moe_workspace_size(MOE_OP_ADAMW, 0, 0, 1, 1, 0, MOE_F32), MOE_ERR_WORKSPACE,
+          "moe_adamw_step: workspace too small");
+  if (n == 0) return MOE_OK;
+  const bool q8 = state_bits == 8;
+  REQUIRE(params != nullptr && grads != nullptr && ms != nullptr && vs != nullptr && numels != nullptr &&
+              weight_decays != nullptr && dtypes != nullptr && lr != nullptr && step != nullptr,
+          MOE_ERR_INVALID_ARG, "moe_adamw_step: a NULL array, lr or step");
+  REQUIRE(q8 == (m_scales != nullptr) && q8 == (v_scales != nullptr), MOE_ERR_INVALID_ARG,
+          "moe_adamw_step: scales go with 8-bit states, and only with them");
+  for (int i = 0; i < n; ++i) {
+    REQUIRE(numels[i] >= 0 && numels[i] <= (1LL << 40), MOE_ERR_INVALID_ARG, "moe_adamw_step: bad numel");
+    REQUIRE(dtype_ok(dtypes[i]), MOE_ERR_INVALID_ARG, "moe_adamw_step: bad dtype");
+    if (numels[i] == 0) continue;
+    REQUIRE_PTR(params[i]); REQUIRE_PTR(grads[i]); REQUIRE_PTR(ms[i]); REQUIRE_PTR(vs[i]);
+    REQUIRE(dtypes[i] == MOE_F32 || (masters != nullptr && masters[i] != nullptr && aligned16(masters[i])),
+            MOE_ERR_INVALID_ARG, "moe_adamw_step: a bf16 parameter needs an aligned fp32 master");
+    REQUIRE(!q8 || (m_scales[i] != nullptr && v_scales[i] != nullptr), MOE_ERR_INVALID_ARG,
+            "moe_adamw_step: an 8-bit state without scales");
+  }
+  const AdamwScalars c{lr, step, grad_scale, status_of(ws), beta1, beta2, log(beta1), log(beta2), eps, seed, q8};
+  AdamwTensor part[kAdamwMaxTensors];
+  for (int i = 0; i < n; i += kAdamwMaxTensors) {
+    const int m = std::min(n - i, kAdamwMaxTensors);
+    for (int j = 0; j < m; ++j) {
+      const int q = i + j;
+      part[j] = AdamwTensor{params[q], grads[q], dtypes[q] == MOE_BF16 ? masters[q] : nullptr, ms[q], vs[q],
+                            q8 ? m_scales[q] : nullptr, q8 ? v_scales[q] : nullptr, (long long)numels[q],
+                            weight_decays[q], dtypes[q]};
+    }
+    launch_adamw(part, m, i, c, (cudaStream_t)stream);
+  }
+  return check_launch("moe_adamw_step");
+}
+
+int moe_quantize_w4(const void* W, int E, int K, int N, int dtype, int group, void* q, void* scale, void* ws,
+                    size_t ws_bytes, void* stream) {
+  REQUIRE(E >= 1 && E <= 1024 && K >= 32 && N >= 32, MOE_ERR_INVALID_ARG,
+          "moe_quantize_w4: need 1 <= E <= 1024, K >= 32, N >= 32");
+  REQUIRE(dtype_ok(dtype), MOE_ERR_INVALID_ARG, "moe_quantize_w4: bad dtype");
+  REQUIRE(group == 32 || group == 64 || group == 128, MOE_ERR_INVALID_ARG, "moe_quantize_w4: group is 32, 64 or 128");
+  REQUIRE(K % 32 == 0 && N % 32 == 0, MOE_ERR_UNSUPPORTED, "moe_quantize_w4: K and N must be multiples of 32");
+  REQUIRE(K <= (1 << 20) && N <= (1 << 20), MOE_ERR_UNSUPPORTED, "moe_quantize_w4: K or N above 2^20");
+  REQUIRE(ws != nullptr && ws_bytes >= sizeof(WsHeader), MOE_ERR_WORKSPACE, "moe_quantize_w4: workspace too small");
+  REQUIRE_PTR(W); REQUIRE_PTR(q); REQUIRE_PTR(scale);
+  launch_quantize_w4(dtype, W, E, K, N, group, q, scale, (cudaStream_t)stream);
+  return check_launch("moe_quantize_w4");
+}
+
+int moe_expert_ffn_w4(const void* x, const float* x_scale, const int32_t* topk_idx, const float* topk_w,
+                      const void* W1q, const void* W1s, const void* W3q, const void* W3s, const void* W2q,
+                      const void* W2s, int T, int k, int E, int h, int f, int group, int x_dtype, int dtype, void* y,
+                      void* ws, size_t ws_bytes, void* stream) {
+  REQUIRE(T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= E && h >= 32 && f >= 32, MOE_ERR_INVALID_ARG,
+          "moe_expert_ffn_w4: need T >= 0, 1 <= k <= E <= 1024, h >= 32, f >= 32");
+  REQUIRE(dtype_ok(dtype), MOE_ERR_INVALID_ARG, "moe_expert_ffn_w4: bad dtype");
+  REQUIRE(x_dtype == dtype || (x_dtype == MOE_E4M3 && dtype == MOE_BF16), MOE_ERR_INVALID_ARG,
+          "moe_expert_ffn_w4: x is of the call's dtype, or e4m3 with bf16 outputs");
+  REQUIRE((x_dtype == MOE_E4M3) == (x_scale != nullptr) || T == 0, MOE_ERR_INVALID_ARG,
+          "moe_expert_ffn_w4: x_scale goes with e4m3 activations, and only with them");
+  REQUIRE(group == 32 || group == 64 || group == 128, MOE_ERR_INVALID_ARG, "moe_expert_ffn_w4: group is 32, 64 or 128");
+  REQUIRE(h % 32 == 0 && f % 32 == 0, MOE_ERR_UNSUPPORTED, "moe_expert_ffn_w4: h and f must be multiples of 32");
+  REQUIRE(h <= (1 << 20) && f <= (1 << 20), MOE_ERR_UNSUPPORTED, "moe_expert_ffn_w4: h or f above 2^20");
+  REQUIRE((long long)T * k <= 65536, MOE_ERR_UNSUPPORTED, "moe_expert_ffn_w4: T*k above 65536");
+  REQUIRE(ws != nullptr && aligned16(ws) && ws_bytes >= moe_workspace_size(MOE_OP_EXPERT_FFN_W4, T, h, E, k, f, dtype),
+          MOE_ERR_WORKSPACE, "moe_expert_ffn_w4: workspace too small");
+  if (T == 0) return MOE_OK;
+  REQUIRE(topk_idx != nullptr && topk_w != nullptr, MOE_ERR_INVALID_ARG, "moe_expert_ffn_w4: topk_idx or topk_w is NULL");
+  REQUIRE_PTR(x); REQUIRE_PTR(W1q); REQUIRE_PTR(W1s); REQUIRE_PTR(W3q);
+  REQUIRE_PTR(W3s); REQUIRE_PTR(W2q); REQUIRE_PTR(W2s); REQUIRE_PTR(y);
+  char* base = static_cast<char*>(ws) + sizeof(WsHeader);
+  const W4Ffn p{x, x_scale, topk_idx, topk_w, W1q, W1s, W3q, W3s, W2q, W2s, T, k, E, h, f, group, y, base,
+                reinterpret_cast<float*>(base + round256((size_t)T * k * f * esize(dtype))), status_of(ws)};
+  launch_expert_ffn_w4(dtype, p, (cudaStream_t)stream);
+  return check_launch("moe_expert_ffn_w4");
 }
 
 }  // extern "C"

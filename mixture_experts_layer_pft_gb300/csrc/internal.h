@@ -94,6 +94,55 @@ int f32tc_expert_ffn(const float* xbuf, const float* x, const int* token_ids, in
                      const float* W1, const float* W3, const float* W2, int Tk, int E, int h, int f, float* ybuf,
                      float* h1, float* h3, float* a, void* scratch, int* status, cudaStream_t st);
 
+// norm.cu -- add + RMSNorm; the backward's scratch holds at most kNormMaxParts partial rows of dgamma
+constexpr int kNormMaxParts = 304;
+constexpr int kNormMaxWidth = 16384;
+void launch_add_rmsnorm(int dtype, const void* x, const void* residual, const float* gamma, float eps, int T, int h, void* s,
+                        void* y, void* q, float* q_scale, float* rstd, cudaStream_t st);
+void launch_add_rmsnorm_bwd(int dtype, const void* dy, const void* s, const float* gamma, const float* rstd,
+                            const void* ds_add, int T, int h, void* ds, float* dgamma, float* partial, cudaStream_t st);
+
+// adamw.cu
+struct AdamwTensor {
+  void* param;
+  const void* grad;
+  float* master;  // bf16 parameters only
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  long long numel;
+  float weight_decay;
+  int dtype;
+};
+struct AdamwScalars {
+  const float* lr;
+  const int* step;
+  const float* grad_scale;
+  int* status;
+  double beta1, beta2, log_beta1, log_beta2, eps;
+  unsigned long long seed;
+  bool q8;
+};
+constexpr int kAdamwMaxTensors = 384;  // of one launch
+void launch_adamw(const AdamwTensor* t, int n, int first_tensor, const AdamwScalars& c, cudaStream_t st);
+
+// w4.cu -- routed experts over 4-bit weights; a ([T*k, f] dtype) and rows ([T*k, h] fp32) are scratch
+struct W4Ffn {
+  const void* x;
+  const float* x_scale;  // e4m3 activations only
+  const int* topk_idx;
+  const float* topk_w;
+  const void *W1q, *W1s, *W3q, *W3s, *W2q, *W2s;
+  int T, k, E, h, f, group;
+  void* y;
+  void* a;
+  float* rows;
+  int* status;
+};
+void launch_expert_ffn_w4(int dtype, const W4Ffn& p, cudaStream_t st);
+void launch_quantize_w4(int dtype, const void* W, int E, int K, int N, int group, void* q, void* scale, cudaStream_t st);
+
 // gemm_tc.cu -- tcgen05/TMEM/TMA grouped GEMMs (bf16; h and f multiples of 128)
 bool tc_supported(int dtype, int h, int f);
 // Token rows of the padding-free buffer: either xbuf itself ([Tk,h]), or, with xbuf null, row p
