@@ -106,15 +106,16 @@ def _p(t):
         raise ValueError("tensor must be on a CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the handle alone: building torch's Stream object costs more than the rest of a call's marshalling
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+    rc = getattr(_lib or lib(), name)(*args)
     if rc != MOE_OK:
         raise MoEError(name, rc, (lib().moe_last_error() or b"").decode())
 
@@ -324,7 +325,7 @@ def _check(t, name, dtype, shape):
     """Refuse a tensor whose type or shape the call would misread (None passes); returns its pointer."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     return _p(t)
 

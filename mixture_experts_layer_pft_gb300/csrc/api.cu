@@ -599,7 +599,7 @@ int moe_add_rmsnorm_bwd(const void* dy, const void* s, const float* gamma, const
   REQUIRE_PTR(dy); REQUIRE_PTR(s); REQUIRE_PTR(gamma); REQUIRE_PTR(rstd); REQUIRE_PTR(ds);
   REQUIRE(aligned16(ds_add), MOE_ERR_INVALID_ARG, "moe_add_rmsnorm_bwd: ds_add not aligned");
   launch_add_rmsnorm_bwd(dtype, dy, s, gamma, rstd, ds_add, T, h, ds, dgamma,
-                         reinterpret_cast<float*>(static_cast<char*>(ws) + sizeof(WsHeader)), st);
+                         reinterpret_cast<float*>(static_cast<char*>(ws) + sizeof(WsHeader)), status_of(ws), st);
   return check_launch("moe_add_rmsnorm_bwd");
 }
 

@@ -100,7 +100,8 @@ constexpr int kNormMaxWidth = 16384;
 void launch_add_rmsnorm(int dtype, const void* x, const void* residual, const float* gamma, float eps, int T, int h, void* s,
                         void* y, void* q, float* q_scale, float* rstd, cudaStream_t st);
 void launch_add_rmsnorm_bwd(int dtype, const void* dy, const void* s, const float* gamma, const float* rstd,
-                            const void* ds_add, int T, int h, void* ds, float* dgamma, float* partial, cudaStream_t st);
+                            const void* ds_add, int T, int h, void* ds, float* dgamma, float* partial, int* status,
+                            cudaStream_t st);
 
 // adamw.cu
 struct AdamwTensor {

@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
@@ -18,6 +19,10 @@ namespace {
 
 constexpr int kMaxVec = 4;       // 16-byte vectors of a row in one thread
 constexpr int kQGroup = 128;     // columns per scale of the 8-bit output
+
+constexpr int kRingElems = 16;     // elements of a row in one thread of the backward's ring kernel
+constexpr int kRingMaxStages = 8;
+constexpr int kRingBytes = 200 * 1024;
 
 struct NormGeom {
   int vpt, tpr, rpb;  // vectors a thread, threads a row, rows a block
@@ -66,22 +71,31 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* 
   const int nvec = h / VN;
   const bool on = t < T_;
   const size_t row = (size_t)t * nvec;
+  // all of the thread's loads before the first store: x and residual may be s itself, so the compiler
+  // keeps the order that is written here
+  uint4 rx[VPT], rr[VPT];
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int v = lt + u * tpr;
+    rx[u] = rr[u] = make_uint4(0, 0, 0, 0);
+    if (on && v < nvec) {
+      rx[u] = reinterpret_cast<const uint4*>(x)[row + v];
+      if (residual != nullptr) rr[u] = reinterpret_cast<const uint4*>(residual)[row + v];
+    }
+  }
   float f[VPT][VN];
   float ss = 0.f;
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int v = lt + u * tpr;
-#pragma unroll
-    for (int i = 0; i < VN; ++i) f[u][i] = 0.f;
-    if (!on || v >= nvec) continue;
-    unpack(reinterpret_cast<const uint4*>(x)[row + v], f[u], T());
+    unpack(rx[u], f[u], T());
     if (residual != nullptr) {
       float r[VN];
-      unpack(reinterpret_cast<const uint4*>(residual)[row + v], r, T());
+      unpack(rr[u], r, T());
 #pragma unroll
       for (int i = 0; i < VN; ++i) f[u][i] += r[i];
       const uint4 o = pack(f[u], T());
-      reinterpret_cast<uint4*>(s)[row + v] = o;
+      if (on && v < nvec) reinterpret_cast<uint4*>(s)[row + v] = o;
       unpack(o, f[u], T());  // the norm is of the stored sum
     }
 #pragma unroll
@@ -119,72 +133,190 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* 
   }
 }
 
-template <typename T, int VPT>
-__global__ void __launch_bounds__(1024) add_rmsnorm_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ s,
-                                                               const float* __restrict__ gamma, const float* __restrict__ rstd,
-                                                               const T* ds_add, int T_, int h, int tpr, int rpb, T* ds,
-                                                               float* __restrict__ partial) {
-  constexpr int VN = Vec<T>::N;
+// The backward of rows that are too wide for two stages of the ring below (fp32 above 8,533 columns): a block takes
+// every gridDim-th row into its registers.
+template <int VPT>
+__global__ void __launch_bounds__(1024) add_rmsnorm_bwd_wide_kernel(const float* __restrict__ dy, const float* __restrict__ s,
+                                                                    const float* __restrict__ gamma,
+                                                                    const float* __restrict__ rstd, const float* ds_add, int T_,
+                                                                    int h, float* ds, float* __restrict__ partial) {
   __shared__ float red[2][32];
-  const int lt = threadIdx.x % tpr, sub = threadIdx.x / tpr;
-  const int nvec = h / VN;
-  float dg[VPT][VN];
+  const int lt = threadIdx.x, tpr = blockDim.x, nvec = h / 4;
+  float4 dg[VPT];
 #pragma unroll
-  for (int u = 0; u < VPT; ++u)
-#pragma unroll
-    for (int i = 0; i < VN; ++i) dg[u][i] = 0.f;
+  for (int u = 0; u < VPT; ++u) dg[u] = make_float4(0.f, 0.f, 0.f, 0.f);
   int turn = 0;
-  for (long long t0 = (long long)blockIdx.x * rpb; t0 < T_; t0 += (long long)gridDim.x * rpb, turn ^= 1) {
-    const int t = (int)t0 + sub;
-    const bool on = t < T_;
-    const size_t row = (size_t)t * nvec;
-    const float rs = on ? rstd[t] : 0.f;
-    float xh[VPT][VN], g[VPT][VN];
+  for (int t = blockIdx.x; t < T_; t += gridDim.x, turn ^= 1) {
+    const size_t row = (size_t)t * h;
+    const float rs = rstd[t];
+    float4 d[VPT], x[VPT];
     float dot = 0.f;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int v = lt + u * tpr;
-      if (!on || v >= nvec) continue;
-      float d[VN];
-      unpack(reinterpret_cast<const uint4*>(dy)[row + v], d, T());
-      unpack(reinterpret_cast<const uint4*>(s)[row + v], xh[u], T());
-#pragma unroll
-      for (int i = 0; i < VN; i += 4) {
-        const float4 w = load4(gamma + (size_t)v * VN + i);
-        g[u][i] = d[i] * w.x; g[u][i + 1] = d[i + 1] * w.y; g[u][i + 2] = d[i + 2] * w.z; g[u][i + 3] = d[i + 3] * w.w;
-      }
-#pragma unroll
-      for (int i = 0; i < VN; ++i) {
-        xh[u][i] *= rs;
-        dg[u][i] = fmaf(d[i], xh[u][i], dg[u][i]);
-        dot = fmaf(g[u][i], xh[u][i], dot);
-      }
+      if (v >= nvec) continue;
+      d[u] = load4(dy + row + v * 4);
+      x[u] = load4(s + row + v * 4);
+      const float4 w = load4(gamma + v * 4);
+      x[u].x *= rs; x[u].y *= rs; x[u].z *= rs; x[u].w *= rs;
+      const float4 p = make_float4(d[u].x * x[u].x, d[u].y * x[u].y, d[u].z * x[u].z, d[u].w * x[u].w);
+      dg[u].x += p.x; dg[u].y += p.y; dg[u].z += p.z; dg[u].w += p.w;
+      dot = fmaf(p.x, w.x, fmaf(p.y, w.y, fmaf(p.z, w.z, fmaf(p.w, w.w, dot))));
     }
     const float mean = row_sum(dot, red[turn], tpr) / (float)h;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int v = lt + u * tpr;
-      if (!on || v >= nvec) continue;
-      float o[VN];
-      if (ds_add != nullptr) {
-        unpack(reinterpret_cast<const uint4*>(ds_add)[row + v], o, T());
-      } else {
-#pragma unroll
-        for (int i = 0; i < VN; ++i) o[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < VN; ++i) o[i] = fmaf(rs, fmaf(-xh[u][i], mean, g[u][i]), o[i]);
-      reinterpret_cast<uint4*>(ds)[row + v] = pack(o, T());
+      if (v >= nvec) continue;
+      const float4 w = load4(gamma + v * 4);
+      float4 o = ds_add != nullptr ? load4(ds_add + row + v * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      o.x = fmaf(rs, fmaf(-x[u].x, mean, d[u].x * w.x), o.x);
+      o.y = fmaf(rs, fmaf(-x[u].y, mean, d[u].y * w.y), o.y);
+      o.z = fmaf(rs, fmaf(-x[u].z, mean, d[u].z * w.z), o.z);
+      o.w = fmaf(rs, fmaf(-x[u].w, mean, d[u].w * w.w), o.w);
+      store4(ds + row + v * 4, o);
     }
   }
-  float* p = partial + ((size_t)blockIdx.x * rpb + sub) * h;
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int v = lt + u * tpr;
+    if (v < nvec) store4(partial + (size_t)blockIdx.x * h + v * 4, dg[u]);
+  }
+}
+
+// The backward over a ring of row groups in shared memory.  One block an SM; its thread 0 keeps `stages` groups of
+// rows (dy, s, ds_add: each a contiguous piece of memory) under way as bulk copies, so that the reduction over a row
+// and the stores never leave HBM idle, and no register waits for a load.  16 elements of a row in a thread; gamma and
+// the thread's columns of dgamma stay in registers over all rows.
+template <typename T, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* dy, const T* s, const float* __restrict__ gamma,
+                                                                       const float* __restrict__ rstd, const T* ds_add, int T_,
+                                                                       int h, int tpr, int rpb, int stages, T* ds,
+                                                                       float* __restrict__ partial, int* status) {
+  constexpr int VN = Vec<T>::N, VPT = kRingElems / VN;
+  extern __shared__ uint4 ring[];
+  __shared__ float red[2][32];
+  __shared__ uint64_t full[kRingMaxStages];
+  __shared__ int give_up;
+  const int lt = threadIdx.x % tpr, sub = threadIdx.x / tpr;
+  const int nvec = h / VN, arrays = ds_add != nullptr ? 3 : 2, slot = rpb * nvec;
+  const long long step = (long long)gridDim.x * rpb, first = (long long)blockIdx.x * rpb;
+  const int turns = (int)((T_ - first + step - 1) / step);
+  auto issue = [&](int i) {
+    const long long t0 = first + i * step;
+    const uint32_t bytes = (uint32_t)(t0 + rpb <= T_ ? rpb : (int)(T_ - t0)) * (uint32_t)nvec * 16u;
+    uint64_t* bar = &full[i % stages];
+    uint4* to = ring + (size_t)(i % stages) * 3 * slot;
+    ptx::mbar_expect_tx(bar, bytes * arrays);
+    ptx::bulk_load(ptx::smem_u32(to), reinterpret_cast<const uint4*>(dy) + t0 * nvec, bytes, bar);
+    ptx::bulk_load(ptx::smem_u32(to + slot), reinterpret_cast<const uint4*>(s) + t0 * nvec, bytes, bar);
+    if (arrays == 3) ptx::bulk_load(ptx::smem_u32(to + 2 * slot), reinterpret_cast<const uint4*>(ds_add) + t0 * nvec, bytes, bar);
+  };
+  if (threadIdx.x == 0) {
+    give_up = 0;
+    for (int i = 0; i < stages; ++i) ptx::mbar_init(&full[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < stages && i < turns; ++i) issue(i);
+  }
+  float w[VPT][VN], dg[VPT][VN];
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int v = lt + u * tpr;
+#pragma unroll
+    for (int i = 0; i < VN; i += 4) {
+      const float4 g = v < nvec ? load4(gamma + (size_t)v * VN + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      w[u][i] = g.x; w[u][i + 1] = g.y; w[u][i + 2] = g.z; w[u][i + 3] = g.w;
+    }
+#pragma unroll
+    for (int i = 0; i < VN; ++i) dg[u][i] = 0.f;
+  }
+  const float inv_h = 1.0f / (float)h;
+  float rs_next = first + sub < T_ ? rstd[first + sub] : 0.f;
+  __syncthreads();
+  bool alive = true;
+  for (int i = 0; i < turns; ++i) {
+    const long long t = first + i * step + sub;
+    const bool on = t < T_;
+    const float rs = rs_next;
+    rs_next = i + 1 < turns && t + step < T_ ? rstd[t + step] : 0.f;
+    const uint4* in = ring + (size_t)(i % stages) * 3 * slot + (size_t)sub * nvec;
+    const bool ok = ptx::mbar_wait(&full[i % stages], (i / stages) & 1, &give_up, status, 0);
+    uint4 rd[VPT], rx[VPT];
+    float dot = 0.f;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const int v = lt + u * tpr;
+      rd[u] = rx[u] = make_uint4(0, 0, 0, 0);
+      if (ok && on && v < nvec) {
+        rd[u] = in[v];
+        rx[u] = in[slot + v];
+      }
+      float d[VN], x[VN];
+      unpack(rd[u], d, T());
+      unpack(rx[u], x, T());
+#pragma unroll
+      for (int c = 0; c < VN; ++c) {
+        const float dx = d[c] * (x[c] * rs);
+        dg[u][c] += dx;
+        dot = fmaf(dx, w[u][c], dot);
+      }
+    }
+    dot = warp_sum(dot);
+    const int warp = threadIdx.x / kWarp, wpr = tpr / kWarp, w0 = warp / wpr * wpr;
+    if (threadIdx.x % kWarp == 0) red[i & 1][warp] = dot;
+    // every thread is past the stage of turn i - 1 here: it may be filled again
+    if (!__syncthreads_and(ok)) {
+      alive = false;
+      break;
+    }
+    if (threadIdx.x == 0 && i > 0 && i - 1 + stages < turns) issue(i - 1 + stages);
+    if (wpr > 1) {
+      dot = 0.f;
+      for (int k = 0; k < wpr; ++k) dot += red[i & 1][w0 + k];
+    }
+    const float mean = dot * inv_h;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const int v = lt + u * tpr;
+      if (!on || v >= nvec) continue;
+      float d[VN], x[VN], o[VN];
+      unpack(rd[u], d, T());
+      unpack(rx[u], x, T());
+      if (arrays == 3) {
+        unpack(in[2 * slot + v], o, T());
+      } else {
+#pragma unroll
+        for (int c = 0; c < VN; ++c) o[c] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < VN; ++c) o[c] = fmaf(rs, fmaf(-(x[c] * rs), mean, d[c] * w[u][c]), o[c]);
+      reinterpret_cast<uint4*>(ds)[t * nvec + v] = pack(o, T());
+    }
+  }
+  if (!alive) {  // copies may still be on their way into this block's shared memory: let them land
+    const unsigned long long t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < 2000000ull) {}
+    return;
+  }
+  // one partial row of dgamma a block: the row groups' columns are added through shared memory
+  float* sums = reinterpret_cast<float*>(ring);
+  if (rpb > 1) __syncthreads();
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int v = lt + u * tpr;
     if (v >= nvec) continue;
+    float* to = rpb > 1 ? sums + (size_t)sub * h : partial + (size_t)blockIdx.x * h;
 #pragma unroll
     for (int i = 0; i < VN; i += 4)
-      store4(p + (size_t)v * VN + i, make_float4(dg[u][i], dg[u][i + 1], dg[u][i + 2], dg[u][i + 3]));
+      store4(to + (size_t)v * VN + i, make_float4(dg[u][i], dg[u][i + 1], dg[u][i + 2], dg[u][i + 3]));
+  }
+  if (rpb > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < h; c += blockDim.x) {
+      float sum = sums[c];
+      for (int r = 1; r < rpb; ++r) sum += sums[(size_t)r * h + c];
+      partial[(size_t)blockIdx.x * h + c] = sum;
+    }
   }
 }
 
@@ -215,21 +347,46 @@ void launch_fwd(const void* x, const void* residual, const float* gamma, float e
   count_launch(st);
 }
 
-int bwd_blocks(int T_, int rpb) {
-  const int need = (T_ + rpb - 1) / rpb, most = kNormMaxParts / rpb;
-  return need < most ? need : most;
+// The ring needs two stages of a row group at least: rows up to 34,128 bytes (all of bf16's, fp32 up to 8,528 columns).
+// Wider rows go through the kernel that loads them into registers.
+template <typename T, int MAXT>
+int launch_ring(const void* dy, const void* s, const float* gamma, const float* rstd, const void* ds_add, int T_, int h,
+                void* ds, float* partial, int tpr, int rpb, int* status, cudaStream_t st) {
+  const int stage = 3 * rpb * h * (int)sizeof(T);
+  int stages = kRingBytes / stage;
+  if (stages > kRingMaxStages) stages = kRingMaxStages;
+  const int need = (T_ + rpb - 1) / rpb, most = num_sms() < kNormMaxParts ? num_sms() : kNormMaxParts;
+  const int blocks = need < most ? need : most;
+  static bool ready[64] = {};  // per device: the attribute is set once
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    cudaFuncSetAttribute(add_rmsnorm_bwd_ring_kernel<T, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (dev >= 0 && dev < 64) ready[dev] = true;
+  }
+  add_rmsnorm_bwd_ring_kernel<T, MAXT><<<blocks, tpr * rpb, (size_t)stages * stage, st>>>(
+      static_cast<const T*>(dy), static_cast<const T*>(s), gamma, rstd, static_cast<const T*>(ds_add), T_, h, tpr, rpb, stages,
+      static_cast<T*>(ds), partial, status);
+  return blocks;
 }
 
 template <typename T>
 void launch_bwd(const void* dy, const void* s, const float* gamma, const float* rstd, const void* ds_add, int T_, int h,
-                void* ds, float* dgamma, float* partial, cudaStream_t st) {
-  const NormGeom g = norm_geom(h / Vec<T>::N);
-  const int blocks = bwd_blocks(T_, g.rpb);
-  add_rmsnorm_bwd_kernel<T, kMaxVec><<<blocks, g.tpr * g.rpb, 0, st>>>(
-      static_cast<const T*>(dy), static_cast<const T*>(s), gamma, rstd, static_cast<const T*>(ds_add), T_, h, g.tpr, g.rpb,
-      static_cast<T*>(ds), partial);
+                void* ds, float* dgamma, float* partial, int* status, cudaStream_t st) {
+  int parts = 0;
+  if (2 * 3 * h * (int)sizeof(T) <= kRingBytes) {
+    const int tpr = ((h + kRingElems - 1) / kRingElems + 31) / 32 * 32, rpb = tpr >= 512 ? 1 : 512 / tpr;
+    parts = tpr <= 512 ? launch_ring<T, 512>(dy, s, gamma, rstd, ds_add, T_, h, ds, partial, tpr, rpb, status, st)
+                       : launch_ring<T, 1024>(dy, s, gamma, rstd, ds_add, T_, h, ds, partial, tpr, rpb, status, st);
+  } else if constexpr (sizeof(T) == 4) {
+    const NormGeom g = norm_geom(h / Vec<T>::N);  // a row a block at these widths
+    parts = T_ < kNormMaxParts ? T_ : kNormMaxParts;
+    add_rmsnorm_bwd_wide_kernel<kMaxVec><<<parts, g.tpr, 0, st>>>(
+        static_cast<const float*>(dy), static_cast<const float*>(s), gamma, rstd, static_cast<const float*>(ds_add), T_, h,
+        static_cast<float*>(ds), partial);
+  }
   count_launch(st);
-  dgamma_kernel<<<(h + 31) / 32, 256, 0, st>>>(partial, blocks * g.rpb, h, dgamma);
+  dgamma_kernel<<<(h + 31) / 32, 256, 0, st>>>(partial, parts, h, dgamma);
   count_launch(st);
 }
 
@@ -242,9 +399,10 @@ void launch_add_rmsnorm(int dtype, const void* x, const void* residual, const fl
 }
 
 void launch_add_rmsnorm_bwd(int dtype, const void* dy, const void* s, const float* gamma, const float* rstd,
-                            const void* ds_add, int T, int h, void* ds, float* dgamma, float* partial, cudaStream_t st) {
-  if (dtype == MOE_BF16) launch_bwd<__nv_bfloat16>(dy, s, gamma, rstd, ds_add, T, h, ds, dgamma, partial, st);
-  else launch_bwd<float>(dy, s, gamma, rstd, ds_add, T, h, ds, dgamma, partial, st);
+                            const void* ds_add, int T, int h, void* ds, float* dgamma, float* partial, int* status,
+                            cudaStream_t st) {
+  if (dtype == MOE_BF16) launch_bwd<__nv_bfloat16>(dy, s, gamma, rstd, ds_add, T, h, ds, dgamma, partial, status, st);
+  else launch_bwd<float>(dy, s, gamma, rstd, ds_add, T, h, ds, dgamma, partial, status, st);
 }
 
 }  // namespace moe
