@@ -413,7 +413,7 @@ int moe_add_rmsnorm_bwd(const void* dy, const void* s, const float* gamma, const
  * seeds and steps give equal states.  All-zero codes and scales are the state before the first step.
  * lr: fp32[1], step: int32[1] (>= 1, the number of this step), grad_scale: fp32[1] or NULL (1), on the
  * device, so that a captured step follows them.  step < 1 sets MOE_STATUS_BAD_INDEX and changes nothing.
- * An element whose g^2 is not finite keeps p, m and v (in 8 bits as they stand for; a new block scale
+ * In the root, v / (1 - beta2^t) counts as 2^-126 at least.  An element whose g^2 is not finite keeps p, m and v (in 8 bits as they stand for; a new block scale
  * may round them again) and sets MOE_STATUS_NOT_FINITE.  0 <= beta1, beta2 < 1; eps > 0.
  */
 int moe_adamw_step(int n, void* const* params, const void* const* grads, float* const* masters, void* const* ms,
