@@ -2,34 +2,49 @@
 //
 //   W[n, i] = (nibble - 8) * scale[n, i / G];  a = silu(W1_e x) * (W3_e x);  y[t] = sum_j w_j W2_e a.
 //
-// With few rows an expert's product is bound by its weights' bytes, so each weight is read once for all
-// rows of its expert, straight from HBM into the registers of the warp that uses it.  The product runs
-// on the tensor cores with the outputs as M = 16 and the token rows as N = 8: the nibbles become bf16
-// (128 + nibble by an OR into the mantissa, minus 136: exact), a group's sum is kept apart in fp32 and
-// scaled once, so no weight is rounded.  fp32 activations go in as their three exact bf16 planes.
+// With few rows an expert's product is bound by its weights' bytes, so each weight goes straight from HBM into the
+// registers of the warp that uses it, once for all rows of a pass.  The product runs on the tensor cores with the outputs
+// as M = 16 and the token rows as N = 8: the nibbles become bf16 (128 + nibble by an OR into the mantissa, minus 136:
+// exact), a group's sum is kept apart in fp32 and scaled once, so no weight is rounded.  Activations go in as exact bf16
+// values or planes of them: x in bf16 or e4m3 as it is, x in fp32 as its three planes, `a` as three (fp32) or two (bf16
+// layers: 16 significant bits) of its fp32 value.  tcgen05 would want the weights unpacked into shared memory, and a
+// group's scale inside them, which rounds; at these row counts the tensor pipe is not what bounds either path.
 //
-// A warp's step is 16 outputs x 128 inputs.  The sum over inputs may run in any order, so lane (g, q)
-// takes for outputs g and g + 8 the G/4 consecutive inputs of each group that are contiguous in its
-// 4-bit row: the weights need no other layout than [output][input / 2].
+// A warp's step is 16 outputs x 128 inputs.  The sum over inputs may run in any order, so lane (g, q) = (lane / 4, lane % 4)
+// takes for outputs g and g + 8 the G/4 consecutive inputs of each group that are contiguous in its 4-bit row: the weights
+// need no other layout than [output][input / 2].  Two nibbles of a word sit 16 bits apart as inputs i and i + 4, so eight
+// activations go in as (0,4) (1,5) (2,6) (3,7); activation planes are stored in that order ("paired" below).
+//
+// Two forms.  Up to 8 tokens and 64 rows ("few"): two launches; token t is column t of every product, warps split the
+// inputs, and the second kernel adds its outputs over all experts in registers, so no row is written but `a`.  Above
+// ("many"): an expert's rows in passes of 32 through shared memory, warps side by side over 128 outputs, experts' output
+// rows to scratch, and a combine.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kTile = 16;       // outputs of a thread block
+constexpr int kTile = 16;       // outputs of a warp
 constexpr int kStep = 128;      // inputs of a warp's step
-constexpr int kRows = 8;        // token rows of one pass over the weights
-constexpr int kList = 512;      // rows of an expert found in one scan
+constexpr int kFewTokens = 8, kFewRows = 64;
+constexpr int kPass = 32;       // rows of one pass of the many form
+constexpr int kTilesN = kPass / 8;
+constexpr int kStages = 3;      // steps of activations in shared memory, many form
 
 struct W4Mat {
   const unsigned char* q;
   const __nv_bfloat16* s;
 };
+
+// Start of the dependent launch as soon as every block of this one runs; wait for the launch this one depends on.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -44,8 +59,31 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t w, int i) {
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), __floats2bfloat162_rn(136.f, 136.f));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// The A operands of a word's two products: w0 of output g, w1 of output g + 8.
+__device__ __forceinline__ void unpack_word(uint32_t w0, uint32_t w1, uint32_t a[2][4]) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    a[half][0] = nibble_pair(w0, 2 * half);
+    a[half][1] = nibble_pair(w1, 2 * half);
+    a[half][2] = nibble_pair(w0, 2 * half + 1);
+    a[half][3] = nibble_pair(w1, 2 * half + 1);
+  }
+}
+// Place of input i of eight in the paired order.
+__device__ __forceinline__ int paired(int i) { return (i & ~7) | ((i & 3) << 1) | ((i >> 2) & 1); }
 
-// Eight consecutive activations as bf16 planes, in the order (0,4) (1,5) (2,6) (3,7) of nibble_pair.
+template <int P>
+__device__ __forceinline__ void split_planes(float v, __nv_bfloat16* out) {
+  out[0] = __float2bfloat16_rn(v);
+#pragma unroll
+  for (int p = 1; p < P; ++p) {
+    v -= __bfloat162float(out[p - 1]);
+    out[p] = __float2bfloat16_rn(v);
+  }
+}
+
+// Eight consecutive activations as paired bf16 planes: from x as the caller has it, or from `a`'s paired planes.
+struct E4M3 { unsigned char v; };
 template <typename X> struct Acts;
 template <> struct Acts<__nv_bfloat16> {
   static constexpr int kPlanes = 1;
@@ -62,15 +100,15 @@ template <> struct Acts<float> {
     const float f[2][4] = {{lo.x, lo.y, lo.z, lo.w}, {hi.x, hi.y, hi.z, hi.w}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      __nv_bfloat162 v[3];
-      split3_value(f[0][i], &v[0].x, &v[1].x, &v[2].x);
-      split3_value(f[1][i], &v[0].y, &v[1].y, &v[2].y);
+      __nv_bfloat16 u[3], v[3];
+      split_planes<3>(f[0][i], u);
+      split_planes<3>(f[1][i], v);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) b[k][i] = *reinterpret_cast<uint32_t*>(&v[k]);
+      for (int k = 0; k < 3; ++k)
+        b[k][i] = (uint32_t)__bfloat16_as_ushort(u[k]) | ((uint32_t)__bfloat16_as_ushort(v[k]) << 16);
     }
   }
 };
-struct E4M3 { unsigned char v; };
 template <> struct Acts<E4M3> {
   static constexpr int kPlanes = 1;
   static __device__ __forceinline__ void load(const E4M3* p, uint32_t b[1][4]) {
@@ -84,14 +122,13 @@ template <> struct Acts<E4M3> {
   }
 };
 
-// One step's weights of outputs `row` (this lane's g; g + 8 follows 8 rows later): 4 words each.
+// One step's 4-bit words of one output (its row q, K inputs): lane quarter `sub` of every group.
 template <int G>
-__device__ __forceinline__ void load_weights(const unsigned char* q, int K, int k0, int lane, uint32_t* w) {
-  const int sub = lane % 4;
+__device__ __forceinline__ void load_words(const unsigned char* q, int K, int k0, int sub, uint32_t* w) {
 #pragma unroll
   for (int i = 0; i < kStep / G; ++i) {
     const int k = k0 + i * G + sub * (G / 4);
-    const bool in = k < K;  // K is a multiple of 32, but a group may be cut short: G / 4 divides it
+    const bool in = k < K;  // K is a multiple of 32: of G / 4 inputs none or all are inside
     const void* p = q + k / 2;
     if constexpr (G == 128) {
       const uint4 u = in ? __ldg(static_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
@@ -105,163 +142,467 @@ __device__ __forceinline__ void load_weights(const unsigned char* q, int K, int 
   }
 }
 
-// acc[m] += the product of MATS matrices' 16 outputs with up to 8 rows, over this warp's steps.
-// `x`: this lane's row (column lane / 4 of the product), null where there is none.  xs0, xs1: the
-// activation scales of columns 2q and 2q + 1 (one per 128 inputs), or null.
-template <typename X, int G, int MATS>
-__device__ __forceinline__ void product(const W4Mat* mats, size_t out0, int K, const X* x, const float* xs0, const float* xs1,
-                                        int warp, int lane, float acc[MATS][4]) {
-  constexpr int P = Acts<X>::kPlanes;
-  const int groups = (K + G - 1) / G;
-  const size_t r0 = out0 + lane / 4, r1 = r0 + 8;
-  for (int k0 = warp * kStep; k0 < K; k0 += kWarps * kStep) {
-    uint32_t w[MATS][2][4];
+// A step's words and scales of MATS matrices' outputs g and g + 8.
+template <int G, int MATS>
+struct Weights {
+  uint32_t w[MATS][2][4];
+  __nv_bfloat16 s[MATS][2][kStep / G];
+
+  __device__ __forceinline__ void load(const W4Mat* mats, size_t out, int K, int k0, int lane) {
+    const int groups = (K + G - 1) / G;
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const size_t row = out + lane / 4 + r * 8;
+        load_words<G>(mats[m].q + row * (K / 2), K, k0, lane % 4, w[m][r]);
+#pragma unroll
+        for (int i = 0; i < kStep / G; ++i)
+          s[m][r][i] = k0 + i * G < K ? mats[m].s[row * groups + k0 / G + i] : __float2bfloat16_rn(0.f);
+      }
+  }
+};
+
+// ------------------------------------------------------------------------------------ few rows
+
+struct FewArgs {
+  const void* x;          // gate/up: [T, K] of X; down: a's planes [P][T*k][K]
+  const float* x_scale;
+  const int* topk_idx;
+  const float* topk_w;
+  int T, k, E, K, N;      // K inputs, N outputs
+  W4Mat mat[2];
+  void* out;              // gate/up: a's planes [P][T*k][N]; down: y [T, N]
+  int* status;
+};
+
+// Rows of topk_idx that name expert e, as bits (at most 64 rows).
+__device__ __forceinline__ unsigned long long rows_of(const int* __restrict__ topk_idx, int rows, int e, int lane) {
+  const bool lo = lane < rows && __ldg(topk_idx + lane) == e;
+  const bool hi = lane + 32 < rows && __ldg(topk_idx + lane + 32) == e;
+  return (unsigned long long)__ballot_sync(0xffffffffu, lo) | ((unsigned long long)__ballot_sync(0xffffffffu, hi) << 32);
+}
+// Of a row mask, token t's bits, moved to bit 0.
+__device__ __forceinline__ unsigned long long bits_of(unsigned long long mask, int t, int k) {
+  return (mask >> (t * k)) & (k < 64 ? (1ull << k) - 1ull : ~0ull);
+}
+
+// part += a step's group (index i) of MATS matrices with the activations at `x` (this lane's column; null: none there).
+template <typename X, int G, int MATS, typename LOAD>
+__device__ __forceinline__ void few_group(const Weights<G, MATS>& w, int i, int k, int K, int lane, LOAD load,
+                                          float part[MATS][4]) {
+  constexpr int P = X::kPlanes;
+#pragma unroll
+  for (int m = 0; m < MATS; ++m)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) part[m][c] = 0.f;
+#pragma unroll
+  for (int j = 0; j < G / 32; ++j) {
+    const int kx = k + (lane % 4) * (G / 4) + j * 8;
+    uint32_t b[P][4];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) b[p][c] = 0u;
+    if (kx < K) load(kx, b);
+    const int word = i * (G / 32) + j;
 #pragma unroll
     for (int m = 0; m < MATS; ++m) {
-      load_weights<G>(mats[m].q + r0 * (K / 2), K, k0, lane, w[m][0]);
-      load_weights<G>(mats[m].q + r1 * (K / 2), K, k0, lane, w[m][1]);
-    }
-    const float s0 = xs0 != nullptr ? __ldg(xs0 + k0 / kStep) : 1.f, s1 = xs1 != nullptr ? __ldg(xs1 + k0 / kStep) : 1.f;
+      uint32_t a[2][4];
+      unpack_word(w.w[m][0][word], w.w[m][1][word], a);
+      if constexpr (P == 1) {
+        mma_bf16(part[m], a[0], b[0][0], b[0][1]);
+        mma_bf16(part[m], a[1], b[0][2], b[0][3]);
+      } else {
+        // the tensor core's sums round towards zero: short chains, the small planes apart, joined in fp32
+        float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kStep / G; ++i) {
-      const int k = k0 + i * G;
-      if (k >= K) break;
-      float part[MATS][4];
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-      for (int m = 0; m < MATS; ++m)
+          for (int p = P - 1; p > 0; --p) mma_bf16(lo, a[half], b[p][2 * half], b[p][2 * half + 1]);
+          mma_bf16(hi, a[half], b[0][2 * half], b[0][2 * half + 1]);
+        }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) part[m][c] = 0.f;
-#pragma unroll
-      for (int j = 0; j < G / 32; ++j) {
-        const int kx = k + (lane % 4) * (G / 4) + j * 8;
-        uint32_t b[P][4];
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) b[p][c] = 0u;
-        if (x != nullptr && kx < K) Acts<X>::load(x + kx, b);
-        const int word = i * (G / 32) + j;
-#pragma unroll
-        for (int m = 0; m < MATS; ++m)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t a[4] = {nibble_pair(w[m][0][word], 2 * half), nibble_pair(w[m][1][word], 2 * half),
-                                   nibble_pair(w[m][0][word], 2 * half + 1), nibble_pair(w[m][1][word], 2 * half + 1)};
-#pragma unroll
-            for (int p = 0; p < P; ++p) mma_bf16(part[m], a, b[p][2 * half], b[p][2 * half + 1]);
-          }
-      }
-#pragma unroll
-      for (int m = 0; m < MATS; ++m) {
-        const float g0 = __bfloat162float(mats[m].s[r0 * groups + k / G]), g1 = __bfloat162float(mats[m].s[r1 * groups + k / G]);
-        acc[m][0] = fmaf(part[m][0], g0 * s0, acc[m][0]);
-        acc[m][1] = fmaf(part[m][1], g0 * s1, acc[m][1]);
-        acc[m][2] = fmaf(part[m][2], g1 * s0, acc[m][2]);
-        acc[m][3] = fmaf(part[m][3], g1 * s1, acc[m][3]);
+        for (int c = 0; c < 4; ++c) part[m][c] += hi[c] + lo[c];
       }
     }
   }
 }
 
-// The rows (t, j) of `e` from topk_idx[pos...], ascending, into list; returns the next position.
-__device__ __forceinline__ int find_rows(const int* __restrict__ topk_idx, int rows, int e, int pos, int* list, int* counts,
-                                         int* found) {
+// `a` of 16 outputs of the slot's expert for the tokens that chose it.  One slot a row of topk_idx: the first row of
+// an expert does them all.
+template <typename X, int PA, int G>
+__global__ void __launch_bounds__(kWarps * 32, 2) w4_few_up_kernel(const __grid_constant__ FewArgs a) {
+  constexpr int AHEAD = 2;
+  __shared__ float red[kWarps][2][kTile][kFewTokens + 1];
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  launch_dependents();
+  const int rows = a.T * a.k;
+  const int e = __ldg(a.topk_idx + blockIdx.y);
+  if ((unsigned)e >= (unsigned)a.E) return;  // flagged by the second kernel
+  const size_t out = (size_t)e * a.N + blockIdx.x * kTile;
+  Weights<G, 2> w[AHEAD];
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d)
+    if ((warp + d * kWarps) * kStep < a.K) w[d].load(a.mat, out, a.K, (warp + d * kWarps) * kStep, lane);
+  const unsigned long long mask = rows_of(a.topk_idx, rows, e, lane);
+  if (__ffsll(mask) - 1 != (int)blockIdx.y) return;  // an earlier row's block does this expert
+  const int col = lane / 4, c0 = (lane % 4) * 2;
+  const bool have = col < a.T && bits_of(mask, col, a.k) != 0;
+  const X* x = static_cast<const X*>(a.x) + (size_t)(have ? col : 0) * a.K;
+  const int xg = (a.K + kStep - 1) / kStep;
+  const float* xs = a.x_scale;
+  float acc[2][4] = {};
+  for (int s = warp; s * kStep < a.K; s += kWarps * AHEAD) {
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) {
+      const int k0 = (s + d * kWarps) * kStep;
+      if (k0 >= a.K) break;
+      float x0 = 1.f, x1 = 1.f;
+      if (xs != nullptr) {
+        x0 = c0 < a.T ? __ldg(xs + c0 * xg + k0 / kStep) : 0.f;
+        x1 = c0 + 1 < a.T ? __ldg(xs + (c0 + 1) * xg + k0 / kStep) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kStep / G; ++i) {
+        float part[2][4];
+        few_group<Acts<X>, G, 2>(w[d], i, k0 + i * G, a.K, lane,
+                                 [&](int kx, uint32_t (*b)[4]) { if (have) Acts<X>::load(x + kx, b); }, part);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float g0 = __bfloat162float(w[d].s[m][0][i]), g1 = __bfloat162float(w[d].s[m][1][i]);
+          acc[m][0] = fmaf(part[m][0], g0 * x0, acc[m][0]);
+          acc[m][1] = fmaf(part[m][1], g0 * x1, acc[m][1]);
+          acc[m][2] = fmaf(part[m][2], g1 * x0, acc[m][2]);
+          acc[m][3] = fmaf(part[m][3], g1 * x1, acc[m][3]);
+        }
+      }
+      const int next = k0 + AHEAD * kWarps * kStep;
+      if (next < a.K) w[d].load(a.mat, out, a.K, next, lane);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) red[warp][m][lane / 4 + (c / 2) * 8][c0 + c % 2] = acc[m][c];
+  __syncthreads();
+  if (threadIdx.x < kTile * kFewTokens) {
+    const int o = threadIdx.x % kTile, t = threadIdx.x / kTile;
+    const unsigned long long mine = t < a.T ? bits_of(mask, t, a.k) : 0;
+    if (mine != 0) {
+      float v[2] = {0.f, 0.f};
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) v[m] += red[q][m][o][t];
+      __nv_bfloat16 plane[PA];
+      split_planes<PA>(v[0] * sigmoidf_(v[0]) * v[1], plane);
+      const size_t row = (size_t)t * a.k + __ffsll(mine) - 1, n = paired(blockIdx.x * kTile + o);
+#pragma unroll
+      for (int p = 0; p < PA; ++p) static_cast<__nv_bfloat16*>(a.out)[((size_t)p * rows + row) * a.N + n] = plane[p];
+    }
+  }
+}
+
+// Paired planes of `a`, `stride` elements apart.
+template <int P> struct Planes {
+  static constexpr int kPlanes = P;
+};
+
+// y of 16 outputs for all tokens: the steps of all experts' products, one after another over the warps.  An expert's
+// row is column t of token t, and joins the token's sum with its weight, so the sum over experts stays in registers.
+template <typename T, int PA, int G>
+__global__ void __launch_bounds__(kWarps * 32, 2) w4_few_down_kernel(const __grid_constant__ FewArgs a) {
+  constexpr int AHEAD = 4;
+  __shared__ float red[kWarps][kTile][kFewTokens + 1];
+  __shared__ int expert[kFewRows], row[kFewRows][kFewTokens], idx[kFewRows];
+  __shared__ float weight[kFewRows][kFewTokens];
+  __shared__ unsigned lead[2];
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int rows = a.T * a.k;
+  // the experts of these tokens, ascending, with each token's row of `a` and weight
+  if (threadIdx.x < kFewRows) idx[threadIdx.x] = threadIdx.x < rows ? __ldg(a.topk_idx + threadIdx.x) : -1;
+  __syncthreads();
+  if (threadIdx.x < kFewRows) {
+    const int e = idx[threadIdx.x];
+    unsigned long long mask = 0, below = 0;
+    for (int r = 0; r < rows; ++r) {
+      mask |= (unsigned long long)(idx[r] == e) << r;
+      below |= (unsigned long long)(idx[r] < e) << r;
+    }
+    const bool in = threadIdx.x < rows && (unsigned)e < (unsigned)a.E;
+    if (threadIdx.x < rows && !in && blockIdx.x == 0) flag_status(a.status, MOE_STATUS_BAD_INDEX);
+    const bool leads = in && __ffsll(mask) - 1 == (int)threadIdx.x;
+    const unsigned ballot = __ballot_sync(0xffffffffu, leads);
+    if (lane == 0) lead[warp] = ballot;
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    if (leads) {
+      const int at = __popcll(below & (lead[0] | (unsigned long long)lead[1] << 32));
+      expert[at] = e;
+      for (int t = 0; t < kFewTokens; ++t) {
+        unsigned long long mine = t < a.T ? bits_of(mask, t, a.k) : 0;
+        row[at][t] = mine != 0 ? t * a.k + __ffsll(mine) - 1 : -1;
+        float sum = 0.f;
+        for (; mine != 0; mine &= mine - 1) sum += __ldg(a.topk_w + t * a.k + __ffsll(mine) - 1);
+        weight[at][t] = sum;
+      }
+    }
+  }
+  __syncthreads();
+  // Warp w takes the steps kb = w - e (mod 8) of expert e, so that a token's sum is the same whatever else is in the batch
+  // (experts that are not its own add zeros), and experts whose steps are no multiple of 8 load the warps evenly.
+  const int S = (a.K + kStep - 1) / kStep, experts = __popc(lead[0]) + __popc(lead[1]);
+  struct Place { int l, kb; };
+  auto enter = [&](Place p) {  // the first step from p on
+    while (p.l < experts && p.kb >= S) {
+      if (++p.l < experts) p.kb = (warp - expert[p.l]) & (kWarps - 1);
+    }
+    return p;
+  };
+  auto first = [&] { return enter(Place{0, experts > 0 ? (warp - expert[0]) & (kWarps - 1) : 0}); };
+  auto after = [&](Place p) { return enter(Place{p.l, p.kb + kWarps}); };
+  Weights<G, 1> w[AHEAD];
+  Place at = first(), ahead = at;  // the step at work, and the next to load
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d)
+    if (ahead.l < experts) {
+      w[d].load(a.mat, (size_t)expert[ahead.l] * a.N + blockIdx.x * kTile, a.K, ahead.kb * kStep, lane);
+      ahead = after(ahead);
+    }
+  wait_dependency();  // `a` is read from here on; the weights above are nobody's output
+  const int col = lane / 4, c0 = (lane % 4) * 2;
+  const size_t plane = (size_t)rows * a.K;
+  float acc[4] = {};
+  while (at.l < experts) {
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) {
+      if (at.l >= experts) break;
+      const int l = at.l, k0 = at.kb * kStep, r = row[l][col];
+      const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + (size_t)(r < 0 ? 0 : r) * a.K;
+      const float x0 = weight[l][c0], x1 = weight[l][c0 + 1];
+#pragma unroll
+      for (int i = 0; i < kStep / G; ++i) {
+        float part[1][4];
+        few_group<Planes<PA>, G, 1>(w[d], i, k0 + i * G, a.K, lane,
+                                    [&](int kx, uint32_t (*b)[4]) {
+                                      if (r < 0) return;
+#pragma unroll
+                                      for (int p = 0; p < PA; ++p) {
+                                        const uint4 u = *reinterpret_cast<const uint4*>(x + p * plane + kx);
+                                        b[p][0] = u.x; b[p][1] = u.y; b[p][2] = u.z; b[p][3] = u.w;
+                                      }
+                                    },
+                                    part);
+        const float g0 = __bfloat162float(w[d].s[0][0][i]), g1 = __bfloat162float(w[d].s[0][1][i]);
+        acc[0] = fmaf(part[0][0] * g0, x0, acc[0]);
+        acc[1] = fmaf(part[0][1] * g0, x1, acc[1]);
+        acc[2] = fmaf(part[0][2] * g1, x0, acc[2]);
+        acc[3] = fmaf(part[0][3] * g1, x1, acc[3]);
+      }
+      if (ahead.l < experts) {
+        w[d].load(a.mat, (size_t)expert[ahead.l] * a.N + blockIdx.x * kTile, a.K, ahead.kb * kStep, lane);
+        ahead = after(ahead);
+      }
+      at = after(at);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) red[warp][lane / 4 + (c / 2) * 8][c0 + c % 2] = acc[c];
+  __syncthreads();
+  if (threadIdx.x < kTile * kFewTokens) {
+    const int o = threadIdx.x % kTile, t = threadIdx.x / kTile;
+    if (t < a.T) {
+      float v = 0.f;
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) v += red[q][o][t];
+      static_cast<T*>(a.out)[(size_t)t * a.N + blockIdx.x * kTile + o] = from_f<T>(v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------ many rows
+
+// x [T, K] to paired bf16 planes [P][T][K].
+template <typename X>
+__global__ void __launch_bounds__(256) w4_planes_kernel(const X* __restrict__ x, long long eights, __nv_bfloat16* __restrict__ out) {
+  constexpr int P = Acts<X>::kPlanes;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  launch_dependents();
+  if (i >= eights) return;
+  uint32_t b[P][4];
+  Acts<X>::load(x + i * 8, b);
+#pragma unroll
+  for (int p = 0; p < P; ++p) reinterpret_cast<uint4*>(out)[p * eights + i] = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
+}
+
+struct ManyArgs {
+  const __nv_bfloat16* x;  // paired planes [P][xrows][K]
+  const float* x_scale;
+  const int* topk_idx;
+  int rows, k, xrows, E, K, N;  // row r of topk_idx reads x's row r / k (gate/up) or r (down: k = 1)
+  W4Mat mat[2];
+  void* out;               // gate/up: a's planes [PA][rows][N]; down: [rows, N] fp32
+};
+
+// Rows number lo .. lo + 31 of expert e, ascending, into list; returns how many there are (the block's 256 threads).
+__device__ __forceinline__ int find_rows(const int* __restrict__ topk_idx, int rows, int e, int lo, int* list, int* counts) {
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   int n = 0;
-  while (pos < rows && n <= kList - kWarps * kWarp) {
+  for (int pos = 0; pos < rows && n < lo + kPass; pos += kWarps * kWarp) {
     const int r = pos + threadIdx.x;
     const bool hit = r < rows && __ldg(topk_idx + r) == e;
     const unsigned ballot = __ballot_sync(0xffffffffu, hit);
     __syncthreads();
     if (lane == 0) counts[warp] = __popc(ballot);
     __syncthreads();
-    int before = n;
+    int at = n + __popc(ballot & ((1u << lane) - 1u)) - lo;
     for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) before += counts[i];
+      if (i < warp) at += counts[i];
       n += counts[i];
     }
-    if (hit) list[before + __popc(ballot & ((1u << lane) - 1u))] = r;
-    pos += kWarps * kWarp;
+    if (hit && at >= 0 && at < kPass) list[at] = r;
   }
   __syncthreads();
-  *found = n;
-  return pos;
+  return min(max(n - lo, 0), kPass);
 }
 
-struct W4Args {
-  const void* x;
-  const float* x_scale;
-  const int* topk_idx;
-  int rows, k, E, K, N;   // K inputs, N outputs
-  W4Mat mat[2];
-  void* out;              // gate/up: a [rows, N]; down: [rows, N] fp32
-};
-
-// GATEUP: out[r] = silu(W1 x[r / k]) * (W3 x[r / k]) in OUT; else out[r] = W2 x[r].
-template <typename X, typename OUT, int G, bool GATEUP>
-__global__ void __launch_bounds__(kWarps * 32) w4_kernel(const __grid_constant__ W4Args a) {
+// A block: 128 outputs of the slot's expert, every gridDim.z-th pass of 32 of its rows.
+template <int P, int PA, int G, bool GATEUP>
+__global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_constant__ ManyArgs a) {
   constexpr int MATS = GATEUP ? 2 : 1;
-  __shared__ int list[kList], counts[kWarps];
-  __shared__ float red[kWarps][MATS][kTile][kRows + 1];
+  constexpr int STAGE = kTilesN * 4 * 32 * P;  // 16-byte pieces: [row tile][word][lane][plane]
+  extern __shared__ uint4 stage[];
+  __shared__ int list[kPass], counts[kWarps];
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  launch_dependents();
+  wait_dependency();
   const bool by_row = a.rows <= a.E;  // one slot a row (the first row of an expert does them all), or a slot an expert
   const int e = by_row ? __ldg(a.topk_idx + blockIdx.y) : (int)blockIdx.y;
   if ((unsigned)e >= (unsigned)a.E) return;  // flagged by the combine
-  const size_t out0 = (size_t)e * a.N + blockIdx.x * kTile;
-  bool leads = !by_row;
-  for (int pos = 0; pos < a.rows;) {
-    int n;
-    pos = find_rows(a.topk_idx, a.rows, e, pos, list, counts, &n);
-    if (!leads && list[0] != (int)blockIdx.y) return;  // the first scan finds this slot's own row at least
-    leads = true;
-    for (int first = 0; first < n; first += kRows) {
-      const int col = first + lane / 4, c0 = first + (lane % 4) * 2;
-      auto source = [&](int i) { return GATEUP ? list[i] / a.k : list[i]; };
-      const X* x = col < n ? static_cast<const X*>(a.x) + (size_t)source(col) * a.K : nullptr;
-      const float *xs0 = nullptr, *xs1 = nullptr;
-      if (a.x_scale != nullptr) {
-        const int xg = (a.K + kStep - 1) / kStep;
-        if (c0 < n) xs0 = a.x_scale + (size_t)source(c0) * xg;
-        if (c0 + 1 < n) xs1 = a.x_scale + (size_t)source(c0 + 1) * xg;
+  if (by_row) {
+    bool earlier = false;
+    for (int r = threadIdx.x; r < (int)blockIdx.y; r += kWarps * kWarp) earlier |= __ldg(a.topk_idx + r) == e;
+    if (__syncthreads_or(earlier)) return;
+  }
+  const int out0 = (blockIdx.x * kWarps + warp) * kTile;
+  const bool live = out0 < a.N;
+  const size_t out = (size_t)e * a.N + out0;
+  const int S = (a.K + kStep - 1) / kStep, xg = S;
+  for (int lo = blockIdx.z * kPass;; lo += gridDim.z * kPass) {
+    const int n = find_rows(a.topk_idx, a.rows, e, lo, list, counts);
+    if (n == 0) return;
+    const int tiles = (n + 7) / 8;
+    auto source = [&](int i) { return GATEUP ? list[i] / a.k : list[i]; };
+    // a step's activations: piece (row, eight) of plane p goes where lane (row % 8, quarter) reads it
+    auto fill = [&](int s) {
+      const uint32_t to = ptx::smem_u32(stage + (s % kStages) * STAGE);
+      for (int i = threadIdx.x; i < tiles * 8 * 16; i += kWarps * 32) {
+        const int r = i / 16, c = i % 16, k = s * kStep + c * 8;
+        const int group = c / (G / 8), quarter = c % (G / 8) / (G / 32), word = group * (G / 32) + c % (G / 32);
+        const bool in = r < n && k < a.K;
+        const __nv_bfloat16* from = a.x + (in ? (size_t)source(r) * a.K + k : 0);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          ptx::cp_async_16(to + (((r / 8 * 4 + word) * P + p) * 32 + r % 8 * 4 + quarter) * 16, from + (size_t)p * a.xrows * a.K,
+                           in ? 16u : 0u);
       }
-      float acc[MATS][4];
+    };
 #pragma unroll
-      for (int m = 0; m < MATS; ++m)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][c] = 0.f;
-      product<X, G, MATS>(a.mat, out0, a.K, x, xs0, xs1, warp, lane, acc);
-      __syncthreads();
-#pragma unroll
-      for (int m = 0; m < MATS; ++m)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) red[warp][m][lane / 4 + (c / 2) * 8][(lane % 4) * 2 + c % 2] = acc[m][c];
-      __syncthreads();
-      if (threadIdx.x < kTile * kRows) {
-        const int o = threadIdx.x % kTile, c = threadIdx.x / kTile;
-        if (first + c < n) {
-          float v[MATS];
-#pragma unroll
-          for (int m = 0; m < MATS; ++m) {
-            v[m] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) v[m] += red[w][m][o][c];
-          }
-          const size_t at = (size_t)list[first + c] * a.N + blockIdx.x * kTile + o;
-          if constexpr (GATEUP) static_cast<OUT*>(a.out)[at] = from_f<OUT>(v[0] * sigmoidf_(v[0]) * v[1]);
-          else static_cast<OUT*>(a.out)[at] = from_f<OUT>(v[0]);
-        }
-      }
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (s < S) fill(s);
+      ptx::cp_async_commit();
     }
-    __syncthreads();
+    Weights<G, MATS> next;
+    if (live) next.load(a.mat, out, a.K, 0, lane);
+    const int c0 = (lane % 4) * 2;
+    float acc[MATS][kTilesN][4];
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+      for (int t = 0; t < kTilesN; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[m][t][c] = 0.f;
+    for (int s = 0; s < S; ++s) {
+      ptx::cp_async_wait<kStages - 2>();
+      __syncthreads();  // the step's activations are there, and the stage before it has been read by all
+      if (s + kStages - 1 < S) fill(s + kStages - 1);
+      ptx::cp_async_commit();
+      const Weights<G, MATS> w = next;
+      if (live && s + 1 < S) next.load(a.mat, out, a.K, (s + 1) * kStep, lane);
+      if (!live) continue;
+      const uint4* b = stage + (s % kStages) * STAGE + lane;
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int i = 0; i < kStep / G; ++i) {
+          uint32_t f[G / 32][2][4];
+#pragma unroll
+          for (int j = 0; j < G / 32; ++j) unpack_word(w.w[m][0][i * (G / 32) + j], w.w[m][1][i * (G / 32) + j], f[j]);
+          const float g0 = __bfloat162float(w.s[m][0][i]), g1 = __bfloat162float(w.s[m][1][i]);
+#pragma unroll
+          for (int t = 0; t < kTilesN; ++t) {
+            if (t >= tiles) break;
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < G / 32; ++j) {
+              float low[4] = {0.f, 0.f, 0.f, 0.f}, high[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int p = P - 1; p >= 0; --p) {
+                const uint4 u = b[((t * 4 + i * (G / 32) + j) * P + p) * 32];
+                // one plane: the group's sum in one chain; more: short chains, the small planes apart (the tensor core's
+                // sums round towards zero)
+                float* to = P == 1 ? part : p > 0 ? low : high;
+                mma_bf16(to, f[j][0], u.x, u.y);
+                mma_bf16(to, f[j][1], u.z, u.w);
+              }
+              if constexpr (P > 1) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) part[c] += high[c] + low[c];
+              }
+            }
+            float x0 = 1.f, x1 = 1.f;
+            if (a.x_scale != nullptr) {
+              x0 = t * 8 + c0 < n ? __ldg(a.x_scale + (size_t)source(t * 8 + c0) * xg + s) : 0.f;
+              x1 = t * 8 + c0 + 1 < n ? __ldg(a.x_scale + (size_t)source(t * 8 + c0 + 1) * xg + s) : 0.f;
+            }
+            acc[m][t][0] = fmaf(part[0], g0 * x0, acc[m][t][0]);
+            acc[m][t][1] = fmaf(part[1], g0 * x1, acc[m][t][1]);
+            acc[m][t][2] = fmaf(part[2], g1 * x0, acc[m][t][2]);
+            acc[m][t][3] = fmaf(part[3], g1 * x1, acc[m][t][3]);
+          }
+        }
+    }
+    if (live) {
+#pragma unroll
+      for (int t = 0; t < kTilesN; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int i = t * 8 + c0 + c % 2, o = out0 + lane / 4 + (c / 2) * 8;
+          if (i >= n) continue;
+          if constexpr (GATEUP) {
+            __nv_bfloat16 plane[PA];
+            const float v = acc[0][t][c];
+            split_planes<PA>(v * sigmoidf_(v) * acc[MATS - 1][t][c], plane);
+#pragma unroll
+            for (int p = 0; p < PA; ++p)
+              static_cast<__nv_bfloat16*>(a.out)[((size_t)p * a.rows + list[i]) * a.N + paired(o)] = plane[p];
+          } else {
+            static_cast<float*>(a.out)[(size_t)list[i] * a.N + o] = acc[0][t][c];
+          }
+        }
+    }
+    if (n < kPass) return;
+    __syncthreads();  // list and the stages are rewritten
   }
 }
 
 // y[t] = sum_j topk_w[t,j] * rows[t*k+j], j ascending; a row of no expert counts as zeros.
 template <typename T>
-__global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict__ rows, const int* __restrict__ topk_idx,
+__global__ void __launch_bounds__(256) w4_combine_kernel(const float* rows, const int* __restrict__ topk_idx,
                                                          const float* __restrict__ topk_w, int k, int E, int h,
                                                          T* __restrict__ y, int* status) {
   const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 4;
+  wait_dependency();
   if (c >= h) return;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < k; ++j) {
@@ -271,7 +612,7 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict
       continue;
     }
     const float w = __ldg(topk_w + r);
-    const float4 v = load4(rows + r * h + c);
+    const float4 v = *reinterpret_cast<const float4*>(rows + r * h + c);
     s.x = fmaf(w, v.x, s.x); s.y = fmaf(w, v.y, s.y); s.z = fmaf(w, v.z, s.z); s.w = fmaf(w, v.w, s.w);
   }
   store4(y + (size_t)t * h + c, s);
@@ -314,38 +655,104 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ 
   }
 }
 
-template <typename X, typename OUT, bool GATEUP>
-void launch_product(const W4Args& a, int G, cudaStream_t st) {
-  const dim3 grid(a.N / kTile, a.rows < a.E ? a.rows : a.E);
-  if (G == 128) w4_kernel<X, OUT, 128, GATEUP><<<grid, kWarps * 32, 0, st>>>(a);
-  else if (G == 64) w4_kernel<X, OUT, 64, GATEUP><<<grid, kWarps * 32, 0, st>>>(a);
-  else w4_kernel<X, OUT, 32, GATEUP><<<grid, kWarps * 32, 0, st>>>(a);
+// A launch that may begin while the one before it on the stream still runs (the kernel waits for it by itself).
+template <typename A>
+void launch_early(void (*kernel)(A), dim3 grid, int threads, size_t bytes, cudaStream_t st, const A& args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args);
   count_launch(st);
 }
 
-template <typename T>
-void run(const W4Ffn& p, cudaStream_t st) {
-  W4Args up{p.x, p.x_scale, p.topk_idx, p.T * p.k, p.k, p.E, p.h, p.f,
-            {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
-             {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, p.a};
-  bool done = false;
-  if constexpr (sizeof(T) == 2) {  // e4m3 activations come with bf16 outputs
-    if ((done = p.x_scale != nullptr)) launch_product<E4M3, T, true>(up, p.group, st);
-  }
-  if (!done) launch_product<T, T, true>(up, p.group, st);
-  W4Args down{p.a, nullptr, p.topk_idx, p.T * p.k, 1, p.E, p.f, p.h,
-              {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.rows};
-  launch_product<T, float, false>(down, p.group, st);
-  w4_combine_kernel<T><<<dim3(p.T, (p.h / 4 + 255) / 256), 256, 0, st>>>(p.rows, p.topk_idx, p.topk_w, p.k, p.E, p.h,
-                                                                        static_cast<T*>(p.y), p.status);
+template <typename T> constexpr int kActPlanes = sizeof(T) == 2 ? 2 : 3;  // planes of `a`
+
+template <typename X, typename T, int G>
+void few(const W4Ffn& p, cudaStream_t st) {
+  constexpr int PA = kActPlanes<T>;
+  const FewArgs up{p.x, p.x_scale, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.h, p.f,
+                   {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
+                    {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, p.a, p.status};
+  w4_few_up_kernel<X, PA, G><<<dim3(p.f / kTile, p.T * p.k), kWarps * 32, 0, st>>>(up);
   count_launch(st);
+  const FewArgs down{p.a, nullptr, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.f, p.h,
+                     {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.y, p.status};
+  launch_early(w4_few_down_kernel<T, PA, G>, dim3(p.h / kTile), kWarps * 32, 0, st, down);
+}
+
+template <int P, int PA, int G, bool GATEUP>
+void many_product(const ManyArgs& a, int tokens, cudaStream_t st) {
+  const int bytes = kStages * kTilesN * 4 * 32 * P * 16;
+  static bool ready[64] = {};  // per device: the attribute is set once
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    cudaFuncSetAttribute(w4_many_kernel<P, PA, G, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (dev >= 0 && dev < 64) ready[dev] = true;
+  }
+  const dim3 grid((a.N + kWarps * kTile - 1) / (kWarps * kTile), a.rows < a.E ? a.rows : a.E,
+                  tokens < 256 ? (tokens + kPass - 1) / kPass : 8);
+  launch_early(w4_many_kernel<P, PA, G, GATEUP>, grid, kWarps * 32, bytes, st, a);
+}
+
+template <typename X, typename T, int G>
+void many(const W4Ffn& p, cudaStream_t st) {
+  constexpr int PX = Acts<X>::kPlanes, PA = kActPlanes<T>;
+  const long long eights = (long long)p.T * p.h / 8;
+  w4_planes_kernel<X><<<(unsigned)((eights + 255) / 256), 256, 0, st>>>(static_cast<const X*>(p.x), eights,
+                                                                       static_cast<__nv_bfloat16*>(p.x_planes));
+  count_launch(st);
+  const ManyArgs up{static_cast<const __nv_bfloat16*>(p.x_planes), p.x_scale, p.topk_idx, p.T * p.k, p.k, p.T, p.E, p.h, p.f,
+                    {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
+                     {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, p.a};
+  many_product<PX, PA, G, true>(up, p.T, st);
+  const ManyArgs down{static_cast<const __nv_bfloat16*>(p.a), nullptr, p.topk_idx, p.T * p.k, 1, p.T * p.k, p.E, p.f, p.h,
+                      {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.rows};
+  many_product<PA, PA, G, false>(down, p.T, st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.T, (p.h / 4 + 255) / 256);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, w4_combine_kernel<T>, (const float*)p.rows, p.topk_idx, p.topk_w, p.k, p.E, p.h, static_cast<T*>(p.y), p.status);
+  count_launch(st);
+}
+
+template <typename X, typename T>
+void run(const W4Ffn& p, cudaStream_t st) {
+  const bool is_few = p.T <= kFewTokens && p.T * p.k <= kFewRows;
+  if (p.group == 128) is_few ? few<X, T, 128>(p, st) : many<X, T, 128>(p, st);
+  else if (p.group == 64) is_few ? few<X, T, 64>(p, st) : many<X, T, 64>(p, st);
+  else is_few ? few<X, T, 32>(p, st) : many<X, T, 32>(p, st);
 }
 
 }  // namespace
 
+size_t w4_scratch(int dtype, long long T, long long k, int h, int f, W4Scratch* at) {
+  auto round = [](size_t b) { return (b + 255) & ~size_t(255); };
+  W4Scratch s;
+  s.a = 0;
+  s.rows = s.a + round((size_t)T * k * f * 2 * (dtype == MOE_BF16 ? 2 : 3));
+  s.x_planes = s.rows + round((size_t)T * k * h * sizeof(float));
+  if (at != nullptr) *at = s;
+  return s.x_planes + round((size_t)T * h * 2 * (dtype == MOE_BF16 ? 1 : 3));
+}
+
 void launch_expert_ffn_w4(int dtype, const W4Ffn& p, cudaStream_t st) {
-  if (dtype == MOE_BF16) run<__nv_bfloat16>(p, st);
-  else run<float>(p, st);
+  if (dtype == MOE_F32) run<float, float>(p, st);
+  else if (p.x_scale != nullptr) run<E4M3, __nv_bfloat16>(p, st);
+  else run<__nv_bfloat16, __nv_bfloat16>(p, st);
 }
 
 void launch_quantize_w4(int dtype, const void* W, int E, int K, int N, int group, void* q, void* scale, cudaStream_t st) {
