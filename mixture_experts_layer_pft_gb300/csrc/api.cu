@@ -674,6 +674,7 @@ int moe_expert_ffn_w4(const void* x, const float* x_scale, const int32_t* topk_i
   REQUIRE(group == 32 || group == 64 || group == 128, MOE_ERR_INVALID_ARG, "moe_expert_ffn_w4: group is 32, 64 or 128");
   REQUIRE(h % 32 == 0 && f % 32 == 0, MOE_ERR_UNSUPPORTED, "moe_expert_ffn_w4: h and f must be multiples of 32");
   REQUIRE(h <= (1 << 20) && f <= (1 << 20), MOE_ERR_UNSUPPORTED, "moe_expert_ffn_w4: h or f above 2^20");
+  REQUIRE((long long)h * f < (1LL << 32), MOE_ERR_UNSUPPORTED, "moe_expert_ffn_w4: h*f at or above 2^32");
   REQUIRE((long long)T * k <= 65536, MOE_ERR_UNSUPPORTED, "moe_expert_ffn_w4: T*k above 65536");
   REQUIRE(ws != nullptr && aligned16(ws) && ws_bytes >= moe_workspace_size(MOE_OP_EXPERT_FFN_W4, T, h, E, k, f, dtype),
           MOE_ERR_WORKSPACE, "moe_expert_ffn_w4: workspace too small");

@@ -15,10 +15,10 @@
 // need no other layout than [output][input / 2].  Two nibbles of a word sit 16 bits apart as inputs i and i + 4, so eight
 // activations go in as (0,4) (1,5) (2,6) (3,7); activation planes are stored in that order ("paired" below).
 //
-// Two forms.  Up to 8 tokens and 64 rows ("few"): two launches; token t is column t of every product, warps split the
+// Two forms.  Up to 8 tokens and 64 rows, as far as their activations fit in shared memory ("few"): two launches; token t is column t of every product, warps split the
 // inputs, and the second kernel adds its outputs over all experts in registers, so no row is written but `a`.  Above
-// ("many"): an expert's rows in passes of 32 through shared memory, warps side by side over 128 outputs, experts' output
-// rows to scratch, and a combine.
+// ("many"): an expert's rows in passes of 32 through shared memory, warps side by side over 64 outputs and two halves of
+// the inputs, experts' output rows to scratch, and a combine.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -35,7 +35,9 @@ constexpr int kStep = 128;      // inputs of a warp's step
 constexpr int kFewTokens = 8, kFewRows = 64;
 constexpr int kPass = 32;       // rows of one pass of the many form
 constexpr int kTilesN = kPass / 8;
-constexpr int kStages = 3;      // steps of activations in shared memory, many form
+constexpr int kManyTiles = 4;   // warps side by side over the outputs, many form
+constexpr int kStages = 3;      // turns of activations in shared memory, many form
+constexpr int kFewBytes = 108 * 1024;  // shared memory for the few form's activations
 
 struct W4Mat {
   const unsigned char* q;
@@ -122,46 +124,86 @@ template <> struct Acts<E4M3> {
   }
 };
 
-// One step's 4-bit words of one output (its row q, K inputs): lane quarter `sub` of every group.
+// A lane's place in a matrix of one expert: byte offset of output g's row and this lane's quarter of a group, and offset of
+// its scales; output g + 8 lies `q8` and `s8` further.  32 bits suffice for an expert's matrix.
 template <int G>
-__device__ __forceinline__ void load_words(const unsigned char* q, int K, int k0, int sub, uint32_t* w) {
-#pragma unroll
-  for (int i = 0; i < kStep / G; ++i) {
-    const int k = k0 + i * G + sub * (G / 4);
-    const bool in = k < K;  // K is a multiple of 32: of G / 4 inputs none or all are inside
-    const void* p = q + k / 2;
-    if constexpr (G == 128) {
-      const uint4 u = in ? __ldg(static_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-    } else if constexpr (G == 64) {
-      const uint2 u = in ? __ldg(static_cast<const uint2*>(p)) : make_uint2(0, 0);
-      w[2 * i] = u.x; w[2 * i + 1] = u.y;
-    } else {
-      w[i] = in ? __ldg(static_cast<const uint32_t*>(p)) : 0u;
-    }
+struct LanePlace {
+  uint32_t q, s, q8, s8;
+  int k;  // first input of this lane in a step's first group
+  __device__ __forceinline__ LanePlace(int out0, int K, int lane) {
+    const uint32_t row = out0 + lane / 4, groups = (K + G - 1) / G;
+    k = (lane % 4) * (G / 4);
+    q = row * (uint32_t)(K / 2) + k / 2;
+    s = row * groups;
+    q8 = 8u * (uint32_t)(K / 2);
+    s8 = 8u * groups;
   }
-}
+};
 
-// A step's words and scales of MATS matrices' outputs g and g + 8.
+// A step's words and scales of MATS matrices' outputs g and g + 8.  Beyond K the words keep what they held: the activations
+// there are zeros, and any nibble is a finite number.
 template <int G, int MATS>
 struct Weights {
-  uint32_t w[MATS][2][4];
+  uint32_t w[MATS][2][4] = {};
   __nv_bfloat16 s[MATS][2][kStep / G];
 
-  __device__ __forceinline__ void load(const W4Mat* mats, size_t out, int K, int k0, int lane) {
-    const int groups = (K + G - 1) / G;
+  __device__ __forceinline__ void load(const W4Mat* mats, const LanePlace<G>& at, int K, int step) {
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const size_t row = out + lane / 4 + r * 8;
-        load_words<G>(mats[m].q + row * (K / 2), K, k0, lane % 4, w[m][r]);
+        const unsigned char* q = mats[m].q + (at.q + r * at.q8 + (uint32_t)step * (kStep / 2));
+        const __nv_bfloat16* sc = mats[m].s + (at.s + r * at.s8 + (uint32_t)step * (kStep / G));
+        uint32_t* to = w[m][r];
 #pragma unroll
-        for (int i = 0; i < kStep / G; ++i)
-          s[m][r][i] = k0 + i * G < K ? mats[m].s[row * groups + k0 / G + i] : __float2bfloat16_rn(0.f);
+        for (int i = 0; i < kStep / G; ++i) {
+          const int k = step * kStep + i * G;
+          if (k + at.k < K) {  // K is a multiple of 32: of a lane's G / 4 inputs none or all are inside
+            if constexpr (G == 128) {
+              const uint4 u = __ldg(reinterpret_cast<const uint4*>(q));
+              to[0] = u.x; to[1] = u.y; to[2] = u.z; to[3] = u.w;
+            } else if constexpr (G == 64) {
+              const uint2 u = __ldg(reinterpret_cast<const uint2*>(q + 32 * i));
+              to[2 * i] = u.x; to[2 * i + 1] = u.y;
+            } else {
+              to[i] = __ldg(reinterpret_cast<const uint32_t*>(q + 16 * i));
+            }
+          }
+          if (G == 128 || i == 0 || k < K) s[m][r][i] = sc[i];
+          else s[m][r][i] = __float2bfloat16_rn(0.f);
+        }
       }
   }
 };
+
+// A group's words (their A operands f) with one column tile of activations, all planes.  One or two planes: one chain of
+// sums a group.  Three (fp32): the small planes in a chain of their own, as the tensor core's sums round towards zero.
+template <int P, int G, typename LOAD>
+__device__ __forceinline__ void group_product(const uint32_t (*f)[2][4], LOAD load, float part[4]) {
+  float low[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) part[c] = 0.f;
+#pragma unroll
+  for (int j = 0; j < G / 32; ++j)
+#pragma unroll
+    for (int p = P - 1; p >= 0; --p) {
+      const uint4 u = load(j, p);
+      float* to = P == 3 && p > 0 ? low : part;
+      mma_bf16(to, f[j][0], u.x, u.y);
+      mma_bf16(to, f[j][1], u.z, u.w);
+    }
+  if constexpr (P == 3) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) part[c] += low[c];
+  }
+}
+
+// Where the eight inputs number c of a step (16 of them) go: the word, and the lane quarter that reads it.
+template <int G>
+__device__ __forceinline__ void place_of(int c, int* word, int* quarter) {
+  *word = c / (G / 8) * (G / 32) + c % (G / 32);
+  *quarter = c % (G / 8) / (G / 32);
+}
 
 // ------------------------------------------------------------------------------------ few rows
 
@@ -187,98 +229,89 @@ __device__ __forceinline__ unsigned long long bits_of(unsigned long long mask, i
   return (mask >> (t * k)) & (k < 64 ? (1ull << k) - 1ull : ~0ull);
 }
 
-// part += a step's group (index i) of MATS matrices with the activations at `x` (this lane's column; null: none there).
-template <typename X, int G, int MATS, typename LOAD>
-__device__ __forceinline__ void few_group(const Weights<G, MATS>& w, int i, int k, int K, int lane, LOAD load,
-                                          float part[MATS][4]) {
-  constexpr int P = X::kPlanes;
-#pragma unroll
-  for (int m = 0; m < MATS; ++m)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) part[m][c] = 0.f;
-#pragma unroll
-  for (int j = 0; j < G / 32; ++j) {
-    const int kx = k + (lane % 4) * (G / 4) + j * 8;
-    uint32_t b[P][4];
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) b[p][c] = 0u;
-    if (kx < K) load(kx, b);
-    const int word = i * (G / 32) + j;
-#pragma unroll
-    for (int m = 0; m < MATS; ++m) {
-      uint32_t a[2][4];
-      unpack_word(w.w[m][0][word], w.w[m][1][word], a);
-      if constexpr (P == 1) {
-        mma_bf16(part[m], a[0], b[0][0], b[0][1]);
-        mma_bf16(part[m], a[1], b[0][2], b[0][3]);
-      } else {
-        // the tensor core's sums round towards zero: short chains, the small planes apart, joined in fp32
-        float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-          for (int p = P - 1; p > 0; --p) mma_bf16(lo, a[half], b[p][2 * half], b[p][2 * half + 1]);
-          mma_bf16(hi, a[half], b[0][2 * half], b[0][2 * half + 1]);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) part[m][c] += hi[c] + lo[c];
-      }
-    }
-  }
-}
-
 // `a` of 16 outputs of the slot's expert for the tokens that chose it.  One slot a row of topk_idx: the first row of
-// an expert does them all.
+// an expert does them all.  The tokens' activations wait in shared memory as paired planes, unpacked once a block (a step
+// with e4m3 ones unpacked by each warp took more instructions for them than for the weights).
 template <typename X, int PA, int G>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_few_up_kernel(const __grid_constant__ FewArgs a) {
-  constexpr int AHEAD = 2;
+  constexpr int AHEAD = 2, P = Acts<X>::kPlanes;
+  extern __shared__ uint4 acts[];  // [step][word][plane][column][quarter], a piece of zeros, then the scales [step][8]
   __shared__ float red[kWarps][2][kTile][kFewTokens + 1];
+  __shared__ int token[kFewTokens];
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   launch_dependents();
-  const int rows = a.T * a.k;
+  const int rows = a.T * a.k, S = (a.K + kStep - 1) / kStep;
   const int e = __ldg(a.topk_idx + blockIdx.y);
   if ((unsigned)e >= (unsigned)a.E) return;  // flagged by the second kernel
-  const size_t out = (size_t)e * a.N + blockIdx.x * kTile;
+  const LanePlace<G> at(blockIdx.x * kTile, a.K, lane);
+  W4Mat mats[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    mats[m].q = a.mat[m].q + (size_t)e * a.N * (a.K / 2);
+    mats[m].s = a.mat[m].s + (size_t)e * a.N * ((a.K + G - 1) / G);
+  }
   Weights<G, 2> w[AHEAD];
 #pragma unroll
   for (int d = 0; d < AHEAD; ++d)
-    if ((warp + d * kWarps) * kStep < a.K) w[d].load(a.mat, out, a.K, (warp + d * kWarps) * kStep, lane);
+    if (warp + d * kWarps < S) w[d].load(mats, at, a.K, warp + d * kWarps);
   const unsigned long long mask = rows_of(a.topk_idx, rows, e, lane);
   if (__ffsll(mask) - 1 != (int)blockIdx.y) return;  // an earlier row's block does this expert
+  const bool mine = lane < a.T && bits_of(mask, lane < a.T ? lane : 0, a.k) != 0;
+  const unsigned chosen = __ballot_sync(0xffffffffu, mine);
+  const int n = __popc(chosen);
+  if (mine) token[__popc(chosen & ((1u << lane) - 1u))] = lane;  // every warp writes the same
+  __syncwarp();
+  const int zeros = S * 4 * P * n * 4;
+  float* scales = reinterpret_cast<float*>(acts + zeros + 1);
+  if (threadIdx.x == 0) acts[zeros] = make_uint4(0, 0, 0, 0);
+  for (int r = 0; r < n; ++r) {
+    const X* x = static_cast<const X*>(a.x) + (size_t)token[r] * a.K;
+    for (int i = threadIdx.x; i < S * 16; i += kWarps * 32) {
+      uint32_t b[P][4] = {};
+      if (i * 8 < a.K) Acts<X>::load(x + i * 8, b);
+      int word, quarter;
+      place_of<G>(i % 16, &word, &quarter);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        acts[((i / 16 * 4 + word) * P + p) * n * 4 + r * 4 + quarter] = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
+    }
+    if (a.x_scale != nullptr)
+      for (int i = threadIdx.x; i < S; i += kWarps * 32) scales[i * 8 + r] = __ldg(a.x_scale + (size_t)token[r] * S + i);
+  }
+  __syncthreads();
+  // lanes of columns without a row read the piece of zeros
   const int col = lane / 4, c0 = (lane % 4) * 2;
-  const bool have = col < a.T && bits_of(mask, col, a.k) != 0;
-  const X* x = static_cast<const X*>(a.x) + (size_t)(have ? col : 0) * a.K;
-  const int xg = (a.K + kStep - 1) / kStep;
-  const float* xs = a.x_scale;
+  const uint4* from = acts + (col < n ? lane : zeros);
+  const int stride = col < n ? n * 4 : 0;
   float acc[2][4] = {};
-  for (int s = warp; s * kStep < a.K; s += kWarps * AHEAD) {
+  for (int s0 = warp; s0 < S; s0 += kWarps * AHEAD) {
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d) {
-      const int k0 = (s + d * kWarps) * kStep;
-      if (k0 >= a.K) break;
+      const int s = s0 + d * kWarps;
+      if (s >= S) break;
       float x0 = 1.f, x1 = 1.f;
-      if (xs != nullptr) {
-        x0 = c0 < a.T ? __ldg(xs + c0 * xg + k0 / kStep) : 0.f;
-        x1 = c0 + 1 < a.T ? __ldg(xs + (c0 + 1) * xg + k0 / kStep) : 0.f;
+      if (sizeof(X) == 1) {  // columns beyond n hold whatever is there, and are not read in the end
+        const float2 xs = *reinterpret_cast<const float2*>(scales + s * 8 + c0);
+        x0 = xs.x;
+        x1 = xs.y;
       }
+      const uint4* b = from + s * 4 * P * stride;
 #pragma unroll
-      for (int i = 0; i < kStep / G; ++i) {
-        float part[2][4];
-        few_group<Acts<X>, G, 2>(w[d], i, k0 + i * G, a.K, lane,
-                                 [&](int kx, uint32_t (*b)[4]) { if (have) Acts<X>::load(x + kx, b); }, part);
+      for (int i = 0; i < kStep / G; ++i)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
+          uint32_t f[G / 32][2][4];
+#pragma unroll
+          for (int j = 0; j < G / 32; ++j) unpack_word(w[d].w[m][0][i * (G / 32) + j], w[d].w[m][1][i * (G / 32) + j], f[j]);
+          float part[4];
+          group_product<P, G>(f, [&](int j, int p) { return b[((i * (G / 32) + j) * P + p) * stride]; }, part);
           const float g0 = __bfloat162float(w[d].s[m][0][i]), g1 = __bfloat162float(w[d].s[m][1][i]);
-          acc[m][0] = fmaf(part[m][0], g0 * x0, acc[m][0]);
-          acc[m][1] = fmaf(part[m][1], g0 * x1, acc[m][1]);
-          acc[m][2] = fmaf(part[m][2], g1 * x0, acc[m][2]);
-          acc[m][3] = fmaf(part[m][3], g1 * x1, acc[m][3]);
+          acc[m][0] = fmaf(part[0], sizeof(X) == 1 ? g0 * x0 : g0, acc[m][0]);
+          acc[m][1] = fmaf(part[1], sizeof(X) == 1 ? g0 * x1 : g0, acc[m][1]);
+          acc[m][2] = fmaf(part[2], sizeof(X) == 1 ? g1 * x0 : g1, acc[m][2]);
+          acc[m][3] = fmaf(part[3], sizeof(X) == 1 ? g1 * x1 : g1, acc[m][3]);
         }
-      }
-      const int next = k0 + AHEAD * kWarps * kStep;
-      if (next < a.K) w[d].load(a.mat, out, a.K, next, lane);
+      if (s + AHEAD * kWarps < S) w[d].load(mats, at, a.K, s + AHEAD * kWarps);
     }
   }
 #pragma unroll
@@ -287,33 +320,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_few_up_kernel(const __grid_
     for (int c = 0; c < 4; ++c) red[warp][m][lane / 4 + (c / 2) * 8][c0 + c % 2] = acc[m][c];
   __syncthreads();
   if (threadIdx.x < kTile * kFewTokens) {
-    const int o = threadIdx.x % kTile, t = threadIdx.x / kTile;
-    const unsigned long long mine = t < a.T ? bits_of(mask, t, a.k) : 0;
-    if (mine != 0) {
+    const int o = threadIdx.x % kTile, c = threadIdx.x / kTile;
+    if (c < n) {
       float v[2] = {0.f, 0.f};
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int q = 0; q < kWarps; ++q) v[m] += red[q][m][o][t];
+        for (int q = 0; q < kWarps; ++q) v[m] += red[q][m][o][c];
       __nv_bfloat16 plane[PA];
       split_planes<PA>(v[0] * sigmoidf_(v[0]) * v[1], plane);
-      const size_t row = (size_t)t * a.k + __ffsll(mine) - 1, n = paired(blockIdx.x * kTile + o);
+      const size_t row = (size_t)token[c] * a.k + __ffsll(bits_of(mask, token[c], a.k)) - 1, o1 = paired(blockIdx.x * kTile + o);
 #pragma unroll
-      for (int p = 0; p < PA; ++p) static_cast<__nv_bfloat16*>(a.out)[((size_t)p * rows + row) * a.N + n] = plane[p];
+      for (int p = 0; p < PA; ++p) static_cast<__nv_bfloat16*>(a.out)[((size_t)p * rows + row) * a.N + o1] = plane[p];
     }
   }
 }
-
-// Paired planes of `a`, `stride` elements apart.
-template <int P> struct Planes {
-  static constexpr int kPlanes = P;
-};
 
 // y of 16 outputs for all tokens: the steps of all experts' products, one after another over the warps.  An expert's
 // row is column t of token t, and joins the token's sum with its weight, so the sum over experts stays in registers.
 template <typename T, int PA, int G>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_few_down_kernel(const __grid_constant__ FewArgs a) {
-  constexpr int AHEAD = 4;
+  constexpr int AHEAD = PA == 2 ? 4 : 2;  // steps of weights under way; three planes leave room for two
   __shared__ float red[kWarps][kTile][kFewTokens + 1];
   __shared__ int expert[kFewRows], row[kFewRows][kFewTokens], idx[kFewRows];
   __shared__ float weight[kFewRows][kFewTokens];
@@ -352,6 +379,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_few_down_kernel(const __gri
   // Warp w takes the steps kb = w - e (mod 8) of expert e, so that a token's sum is the same whatever else is in the batch
   // (experts that are not its own add zeros), and experts whose steps are no multiple of 8 load the warps evenly.
   const int S = (a.K + kStep - 1) / kStep, experts = __popc(lead[0]) + __popc(lead[1]);
+  const LanePlace<G> at(blockIdx.x * kTile, a.K, lane);
   struct Place { int l, kb; };
   auto enter = [&](Place p) {  // the first step from p on
     while (p.l < experts && p.kb >= S) {
@@ -359,51 +387,79 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_few_down_kernel(const __gri
     }
     return p;
   };
-  auto first = [&] { return enter(Place{0, experts > 0 ? (warp - expert[0]) & (kWarps - 1) : 0}); };
   auto after = [&](Place p) { return enter(Place{p.l, p.kb + kWarps}); };
+  auto load = [&](Place p, Weights<G, 1>& to) {
+    const W4Mat mat{a.mat[0].q + (size_t)expert[p.l] * a.N * (a.K / 2), a.mat[0].s + (size_t)expert[p.l] * a.N * ((a.K + G - 1) / G)};
+    to.load(&mat, at, a.K, p.kb);
+  };
   Weights<G, 1> w[AHEAD];
-  Place at = first(), ahead = at;  // the step at work, and the next to load
+  Place now = enter(Place{0, experts > 0 ? (warp - expert[0]) & (kWarps - 1) : 0}), ahead = now;
 #pragma unroll
   for (int d = 0; d < AHEAD; ++d)
     if (ahead.l < experts) {
-      w[d].load(a.mat, (size_t)expert[ahead.l] * a.N + blockIdx.x * kTile, a.K, ahead.kb * kStep, lane);
+      load(ahead, w[d]);
       ahead = after(ahead);
     }
   wait_dependency();  // `a` is read from here on; the weights above are nobody's output
   const int col = lane / 4, c0 = (lane % 4) * 2;
   const size_t plane = (size_t)rows * a.K;
+  // A step's activations, loaded a step ahead.  Columns without a row keep zeros; they are set where the expert changes.
+  uint4 b[2][4][PA];
+  auto fetch = [&](Place p, bool other_expert, uint4 (*to)[PA]) {
+    const int r = row[p.l][col];
+    if (other_expert) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < PA; ++q) to[i][q] = make_uint4(0, 0, 0, 0);
+    }
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + (size_t)(r < 0 ? 0 : r) * a.K + p.kb * kStep + at.k;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = i / (G / 32) * G + i % (G / 32) * 8;
+      if (r >= 0 && p.kb * kStep + at.k + k < a.K) {
+#pragma unroll
+        for (int q = 0; q < PA; ++q) to[i][q] = *reinterpret_cast<const uint4*>(x + q * plane + k);
+      } else if (r >= 0) {
+#pragma unroll
+        for (int q = 0; q < PA; ++q) to[i][q] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
   float acc[4] = {};
-  while (at.l < experts) {
+  int filled[2] = {-1, -1};  // the expert that each buffer's zeros are of
+  if (now.l < experts) {
+    fetch(now, true, b[0]);
+    filled[0] = now.l;
+  }
+  while (now.l < experts) {
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d) {
-      if (at.l >= experts) break;
-      const int l = at.l, k0 = at.kb * kStep, r = row[l][col];
-      const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + (size_t)(r < 0 ? 0 : r) * a.K;
-      const float x0 = weight[l][c0], x1 = weight[l][c0 + 1];
+      if (now.l >= experts) break;
+      const Place next = after(now);
+      if (next.l < experts) {
+        fetch(next, next.l != filled[(d + 1) & 1], b[(d + 1) & 1]);
+        filled[(d + 1) & 1] = next.l;
+      }
+      const float x0 = weight[now.l][c0], x1 = weight[now.l][c0 + 1];
 #pragma unroll
       for (int i = 0; i < kStep / G; ++i) {
-        float part[1][4];
-        few_group<Planes<PA>, G, 1>(w[d], i, k0 + i * G, a.K, lane,
-                                    [&](int kx, uint32_t (*b)[4]) {
-                                      if (r < 0) return;
+        uint32_t f[G / 32][2][4];
 #pragma unroll
-                                      for (int p = 0; p < PA; ++p) {
-                                        const uint4 u = *reinterpret_cast<const uint4*>(x + p * plane + kx);
-                                        b[p][0] = u.x; b[p][1] = u.y; b[p][2] = u.z; b[p][3] = u.w;
-                                      }
-                                    },
-                                    part);
+        for (int j = 0; j < G / 32; ++j) unpack_word(w[d].w[0][0][i * (G / 32) + j], w[d].w[0][1][i * (G / 32) + j], f[j]);
+        float part[4];
+        group_product<PA, G>(f, [&](int j, int p) { return b[d & 1][i * (G / 32) + j][p]; }, part);
         const float g0 = __bfloat162float(w[d].s[0][0][i]), g1 = __bfloat162float(w[d].s[0][1][i]);
-        acc[0] = fmaf(part[0][0] * g0, x0, acc[0]);
-        acc[1] = fmaf(part[0][1] * g0, x1, acc[1]);
-        acc[2] = fmaf(part[0][2] * g1, x0, acc[2]);
-        acc[3] = fmaf(part[0][3] * g1, x1, acc[3]);
+        acc[0] = fmaf(part[0], g0 * x0, acc[0]);
+        acc[1] = fmaf(part[1], g0 * x1, acc[1]);
+        acc[2] = fmaf(part[2], g1 * x0, acc[2]);
+        acc[3] = fmaf(part[3], g1 * x1, acc[3]);
       }
       if (ahead.l < experts) {
-        w[d].load(a.mat, (size_t)expert[ahead.l] * a.N + blockIdx.x * kTile, a.K, ahead.kb * kStep, lane);
+        load(ahead, w[d]);
         ahead = after(ahead);
       }
-      at = after(at);
+      now = next;
     }
   }
 #pragma unroll
@@ -466,14 +522,15 @@ __device__ __forceinline__ int find_rows(const int* __restrict__ topk_idx, int r
   return min(max(n - lo, 0), kPass);
 }
 
-// A block: 128 outputs of the slot's expert, every gridDim.z-th pass of 32 of its rows.
-template <int P, int PA, int G, bool GATEUP>
-__global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_constant__ ManyArgs a) {
+// A block: 64 outputs of the slot's expert, every gridDim.z-th pass of 32 of its rows.  Warps 0-3 take the even steps of 16
+// outputs each, warps 4-7 the odd ones; a turn of the loop is a step of each.
+template <int P, int PA, int G, bool GATEUP, bool SCALED>
+__global__ void __launch_bounds__(kWarps * 32, P == 3 ? 1 : 2) w4_many_kernel(const __grid_constant__ ManyArgs a) {
   constexpr int MATS = GATEUP ? 2 : 1;
-  constexpr int STAGE = kTilesN * 4 * 32 * P;  // 16-byte pieces: [row tile][word][lane][plane]
-  extern __shared__ uint4 stage[];
+  constexpr int STEP = kTilesN * 4 * 32 * P;  // 16-byte pieces of a step: [row tile][word][plane][lane]
+  extern __shared__ uint4 stage[];            // [stage][half][STEP]
   __shared__ int list[kPass], counts[kWarps];
-  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, half = warp / kManyTiles;
   launch_dependents();
   wait_dependency();
   const bool by_row = a.rows <= a.E;  // one slot a row (the first row of an expert does them all), or a slot an expert
@@ -484,36 +541,43 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_co
     for (int r = threadIdx.x; r < (int)blockIdx.y; r += kWarps * kWarp) earlier |= __ldg(a.topk_idx + r) == e;
     if (__syncthreads_or(earlier)) return;
   }
-  const int out0 = (blockIdx.x * kWarps + warp) * kTile;
+  const int out0 = (blockIdx.x * kManyTiles + warp % kManyTiles) * kTile;
   const bool live = out0 < a.N;
-  const size_t out = (size_t)e * a.N + out0;
-  const int S = (a.K + kStep - 1) / kStep, xg = S;
+  const LanePlace<G> at(live ? out0 : 0, a.K, lane);
+  W4Mat mats[MATS];
+#pragma unroll
+  for (int m = 0; m < MATS; ++m) {
+    mats[m].q = a.mat[m].q + (size_t)e * a.N * (a.K / 2);
+    mats[m].s = a.mat[m].s + (size_t)e * a.N * ((a.K + G - 1) / G);
+  }
+  const int S = (a.K + kStep - 1) / kStep, turns = (S + 1) / 2;
   for (int lo = blockIdx.z * kPass;; lo += gridDim.z * kPass) {
     const int n = find_rows(a.topk_idx, a.rows, e, lo, list, counts);
     if (n == 0) return;
     const int tiles = (n + 7) / 8;
     auto source = [&](int i) { return GATEUP ? list[i] / a.k : list[i]; };
-    // a step's activations: piece (row, eight) of plane p goes where lane (row % 8, quarter) reads it
-    auto fill = [&](int s) {
-      const uint32_t to = ptx::smem_u32(stage + (s % kStages) * STAGE);
-      for (int i = threadIdx.x; i < tiles * 8 * 16; i += kWarps * 32) {
-        const int r = i / 16, c = i % 16, k = s * kStep + c * 8;
-        const int group = c / (G / 8), quarter = c % (G / 8) / (G / 32), word = group * (G / 32) + c % (G / 32);
+    // a turn's activations: piece (row, eight) of plane p goes where lane (row % 8, quarter) reads it
+    auto fill = [&](int turn) {
+      const uint32_t to = ptx::smem_u32(stage + turn % kStages * 2 * STEP);
+      for (int i = threadIdx.x; i < tiles * 8 * 32; i += kWarps * 32) {
+        const int r = i / 32, c = i % 32, k = turn * 2 * kStep + c * 8;
+        int word, quarter;
+        place_of<G>(c % 16, &word, &quarter);
         const bool in = r < n && k < a.K;
         const __nv_bfloat16* from = a.x + (in ? (size_t)source(r) * a.K + k : 0);
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          ptx::cp_async_16(to + (((r / 8 * 4 + word) * P + p) * 32 + r % 8 * 4 + quarter) * 16, from + (size_t)p * a.xrows * a.K,
-                           in ? 16u : 0u);
+          ptx::cp_async_16(to + (c / 16 * STEP + ((r / 8 * 4 + word) * P + p) * 32 + r % 8 * 4 + quarter) * 16,
+                           from + (size_t)p * a.xrows * a.K, in ? 16u : 0u);
       }
     };
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-      if (s < S) fill(s);
+    for (int t = 0; t < kStages - 1; ++t) {
+      if (t < turns) fill(t);
       ptx::cp_async_commit();
     }
     Weights<G, MATS> next;
-    if (live) next.load(a.mat, out, a.K, 0, lane);
+    if (half < S) next.load(mats, at, a.K, half);
     const int c0 = (lane % 4) * 2;
     float acc[MATS][kTilesN][4];
 #pragma unroll
@@ -522,15 +586,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_co
       for (int t = 0; t < kTilesN; ++t)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[m][t][c] = 0.f;
-    for (int s = 0; s < S; ++s) {
+    for (int turn = 0; turn < turns; ++turn) {
       ptx::cp_async_wait<kStages - 2>();
-      __syncthreads();  // the step's activations are there, and the stage before it has been read by all
-      if (s + kStages - 1 < S) fill(s + kStages - 1);
+      __syncthreads();  // the turn's activations are there, and the stage before it has been read by all
+      if (turn + kStages - 1 < turns) fill(turn + kStages - 1);
       ptx::cp_async_commit();
+      const int s = turn * 2 + half;
       const Weights<G, MATS> w = next;
-      if (live && s + 1 < S) next.load(a.mat, out, a.K, (s + 1) * kStep, lane);
-      if (!live) continue;
-      const uint4* b = stage + (s % kStages) * STAGE + lane;
+      if (s + 2 < S) next.load(mats, at, a.K, s + 2);
+      if (s >= S) continue;
+      const uint4* b = stage + (turn % kStages * 2 + half) * STEP + lane;
 #pragma unroll
       for (int m = 0; m < MATS; ++m)
 #pragma unroll
@@ -542,52 +607,46 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_co
 #pragma unroll
           for (int t = 0; t < kTilesN; ++t) {
             if (t >= tiles) break;
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < G / 32; ++j) {
-              float low[4] = {0.f, 0.f, 0.f, 0.f}, high[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int p = P - 1; p >= 0; --p) {
-                const uint4 u = b[((t * 4 + i * (G / 32) + j) * P + p) * 32];
-                // one plane: the group's sum in one chain; more: short chains, the small planes apart (the tensor core's
-                // sums round towards zero)
-                float* to = P == 1 ? part : p > 0 ? low : high;
-                mma_bf16(to, f[j][0], u.x, u.y);
-                mma_bf16(to, f[j][1], u.z, u.w);
-              }
-              if constexpr (P > 1) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) part[c] += high[c] + low[c];
-              }
-            }
+            float part[4];
+            group_product<P, G>(f, [&](int j, int p) { return b[((t * 4 + i * (G / 32) + j) * P + p) * 32]; }, part);
             float x0 = 1.f, x1 = 1.f;
-            if (a.x_scale != nullptr) {
-              x0 = t * 8 + c0 < n ? __ldg(a.x_scale + (size_t)source(t * 8 + c0) * xg + s) : 0.f;
-              x1 = t * 8 + c0 + 1 < n ? __ldg(a.x_scale + (size_t)source(t * 8 + c0 + 1) * xg + s) : 0.f;
+            if constexpr (SCALED) {
+              x0 = t * 8 + c0 < n ? __ldg(a.x_scale + (size_t)source(t * 8 + c0) * S + s) : 0.f;
+              x1 = t * 8 + c0 + 1 < n ? __ldg(a.x_scale + (size_t)source(t * 8 + c0 + 1) * S + s) : 0.f;
             }
-            acc[m][t][0] = fmaf(part[0], g0 * x0, acc[m][t][0]);
-            acc[m][t][1] = fmaf(part[1], g0 * x1, acc[m][t][1]);
-            acc[m][t][2] = fmaf(part[2], g1 * x0, acc[m][t][2]);
-            acc[m][t][3] = fmaf(part[3], g1 * x1, acc[m][t][3]);
+            acc[m][t][0] = fmaf(part[0], SCALED ? g0 * x0 : g0, acc[m][t][0]);
+            acc[m][t][1] = fmaf(part[1], SCALED ? g0 * x1 : g0, acc[m][t][1]);
+            acc[m][t][2] = fmaf(part[2], SCALED ? g1 * x0 : g1, acc[m][t][2]);
+            acc[m][t][3] = fmaf(part[3], SCALED ? g1 * x1 : g1, acc[m][t][3]);
           }
         }
     }
-    if (live) {
+    // the halves' sums meet through shared memory: [warp of the first half][value][lane]
+    ptx::cp_async_wait<0>();
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(stage) + (warp % kManyTiles) * MATS * kTilesN * 4 * 32 + lane;
+    if (half == 1) {
+#pragma unroll
+      for (int v = 0; v < MATS * kTilesN * 4; ++v) sums[v * 32] = acc[v / (kTilesN * 4)][v / 4 % kTilesN][v % 4];
+    }
+    __syncthreads();
+    if (half == 0 && live) {
 #pragma unroll
       for (int t = 0; t < kTilesN; ++t)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int i = t * 8 + c0 + c % 2, o = out0 + lane / 4 + (c / 2) * 8;
           if (i >= n) continue;
+          const float v = acc[0][t][c] + sums[(t * 4 + c) * 32];
           if constexpr (GATEUP) {
             __nv_bfloat16 plane[PA];
-            const float v = acc[0][t][c];
-            split_planes<PA>(v * sigmoidf_(v) * acc[MATS - 1][t][c], plane);
+            const float u = acc[MATS - 1][t][c] + sums[((MATS - 1) * kTilesN * 4 + t * 4 + c) * 32];
+            split_planes<PA>(v * sigmoidf_(v) * u, plane);
 #pragma unroll
             for (int p = 0; p < PA; ++p)
               static_cast<__nv_bfloat16*>(a.out)[((size_t)p * a.rows + list[i]) * a.N + paired(o)] = plane[p];
           } else {
-            static_cast<float*>(a.out)[(size_t)list[i] * a.N + o] = acc[0][t][c];
+            static_cast<float*>(a.out)[(size_t)list[i] * a.N + o] = v;
           }
         }
     }
@@ -674,32 +733,46 @@ void launch_early(void (*kernel)(A), dim3 grid, int threads, size_t bytes, cudaS
 
 template <typename T> constexpr int kActPlanes = sizeof(T) == 2 ? 2 : 3;  // planes of `a`
 
+// Shared memory of the few form's first kernel with T rows.
+template <typename X>
+size_t few_bytes(int T, int K) {
+  const size_t S = (K + kStep - 1) / kStep;
+  return (S * 16 * Acts<X>::kPlanes * T + 1) * 16 + S * 8 * sizeof(float);
+}
+
+template <typename K>
+void allow_shared(K kernel, int bytes, bool* ready) {  // per device: the attribute is set once
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (dev >= 0 && dev < 64) ready[dev] = true;
+  }
+}
+
 template <typename X, typename T, int G>
 void few(const W4Ffn& p, cudaStream_t st) {
   constexpr int PA = kActPlanes<T>;
   const FewArgs up{p.x, p.x_scale, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.h, p.f,
                    {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
                     {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, p.a, p.status};
-  w4_few_up_kernel<X, PA, G><<<dim3(p.f / kTile, p.T * p.k), kWarps * 32, 0, st>>>(up);
+  static bool ready[64] = {};
+  allow_shared(w4_few_up_kernel<X, PA, G>, kFewBytes, ready);
+  w4_few_up_kernel<X, PA, G><<<dim3(p.f / kTile, p.T * p.k), kWarps * 32, few_bytes<X>(p.T, p.h), st>>>(up);
   count_launch(st);
   const FewArgs down{p.a, nullptr, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.f, p.h,
                      {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.y, p.status};
   launch_early(w4_few_down_kernel<T, PA, G>, dim3(p.h / kTile), kWarps * 32, 0, st, down);
 }
 
-template <int P, int PA, int G, bool GATEUP>
+template <int P, int PA, int G, bool GATEUP, bool SCALED>
 void many_product(const ManyArgs& a, int tokens, cudaStream_t st) {
-  const int bytes = kStages * kTilesN * 4 * 32 * P * 16;
-  static bool ready[64] = {};  // per device: the attribute is set once
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !ready[dev]) {
-    cudaFuncSetAttribute(w4_many_kernel<P, PA, G, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (dev >= 0 && dev < 64) ready[dev] = true;
-  }
-  const dim3 grid((a.N + kWarps * kTile - 1) / (kWarps * kTile), a.rows < a.E ? a.rows : a.E,
+  const int bytes = kStages * 2 * kTilesN * 4 * 32 * P * 16;
+  static bool ready[64] = {};
+  allow_shared(w4_many_kernel<P, PA, G, GATEUP, SCALED>, bytes, ready);
+  const dim3 grid((a.N + kManyTiles * kTile - 1) / (kManyTiles * kTile), a.rows < a.E ? a.rows : a.E,
                   tokens < 256 ? (tokens + kPass - 1) / kPass : 8);
-  launch_early(w4_many_kernel<P, PA, G, GATEUP>, grid, kWarps * 32, bytes, st, a);
+  launch_early(w4_many_kernel<P, PA, G, GATEUP, SCALED>, grid, kWarps * 32, bytes, st, a);
 }
 
 template <typename X, typename T, int G>
@@ -712,10 +785,10 @@ void many(const W4Ffn& p, cudaStream_t st) {
   const ManyArgs up{static_cast<const __nv_bfloat16*>(p.x_planes), p.x_scale, p.topk_idx, p.T * p.k, p.k, p.T, p.E, p.h, p.f,
                     {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
                      {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, p.a};
-  many_product<PX, PA, G, true>(up, p.T, st);
+  many_product<PX, PA, G, true, sizeof(X) == 1>(up, p.T, st);
   const ManyArgs down{static_cast<const __nv_bfloat16*>(p.a), nullptr, p.topk_idx, p.T * p.k, 1, p.T * p.k, p.E, p.f, p.h,
                       {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.rows};
-  many_product<PA, PA, G, false>(down, p.T, st);
+  many_product<PA, PA, G, false, false>(down, p.T, st);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.T, (p.h / 4 + 255) / 256);
   cfg.blockDim = dim3(256);
@@ -731,7 +804,7 @@ void many(const W4Ffn& p, cudaStream_t st) {
 
 template <typename X, typename T>
 void run(const W4Ffn& p, cudaStream_t st) {
-  const bool is_few = p.T <= kFewTokens && p.T * p.k <= kFewRows;
+  const bool is_few = p.T <= kFewTokens && p.T * p.k <= kFewRows && few_bytes<X>(p.T, p.h) <= (size_t)kFewBytes;
   if (p.group == 128) is_few ? few<X, T, 128>(p, st) : many<X, T, 128>(p, st);
   else if (p.group == 64) is_few ? few<X, T, 64>(p, st) : many<X, T, 64>(p, st);
   else is_few ? few<X, T, 32>(p, st) : many<X, T, 32>(p, st);
