@@ -37,7 +37,9 @@ constexpr int kPass = 32;       // rows of one pass of the many form
 constexpr int kTilesN = kPass / 8;
 constexpr int kManyTiles = 4;   // warps side by side over the outputs, many form
 constexpr int kStages = 3;      // turns of activations in shared memory, many form
-constexpr int kFewBytes = 108 * 1024;  // shared memory for the few form's activations
+constexpr int kFewBytes = 100 * 1024;  // shared memory for the few form's activations
+constexpr int kFewSteps = 128;         // of a warp: kFewBytes / (128 inputs x 2.25 bytes) / 8, and one more an expert
+constexpr int kUpBlocks = 3, kUpAhead = 1, kDownBlocks = 3, kDownAhead = 2;  // one token: blocks an SM, steps under way
 
 struct W4Mat {
   const unsigned char* q;
@@ -207,14 +209,23 @@ __device__ __forceinline__ void place_of(int c, int* word, int* quarter) {
 
 // ------------------------------------------------------------------------------------ few rows
 
+// With one or two rows an expert the tensor cores would be fed mostly zeros, and making bf16 of the nibbles (11
+// instructions for 8) is what takes the time.  Here the nibbles stay integers: 8 inputs' nibbles become two words of signed
+// bytes 16 * (nibble - 8) in three instructions, and dp4a adds their products with the activations.  Those are integers
+// too, of 16 bits (bf16 and e4m3 activations) or 24 (fp32), as P signed bytes, with one fp32 scale per 16 inputs: an
+// activation is off by at most 2^-16 (2^-24) of the largest of its 16, far below what the output's type can show.
+// Sums of 16 products are exact in 32 bits.
+
 struct FewArgs {
-  const void* x;          // gate/up: [T, K] of X; down: a's planes [P][T*k][K]
+  const void* x;          // gate/up: [T, K] of X; down: nothing
   const float* x_scale;
   const int* topk_idx;
   const float* topk_w;
   int T, k, E, K, N;      // K inputs, N outputs
   W4Mat mat[2];
-  void* out;              // gate/up: a's planes [P][T*k][N]; down: y [T, N]
+  unsigned char* bytes;   // `a` as integers: [T*k][f/16][P][16]
+  float* scales;          // and its scales: [T*k][f/16]
+  void* y;                // down: y [T, N]
   int* status;
 };
 
@@ -229,124 +240,279 @@ __device__ __forceinline__ unsigned long long bits_of(unsigned long long mask, i
   return (mask >> (t * k)) & (k < 64 ? (1ull << k) - 1ull : ~0ull);
 }
 
-// `a` of 16 outputs of the slot's expert for the tokens that chose it.  One slot a row of topk_idx: the first row of
-// an expert does them all.  The tokens' activations wait in shared memory as paired planes, unpacked once a block (a step
-// with e4m3 ones unpacked by each warp took more instructions for them than for the weights).
-template <typename X, int PA, int G>
-__global__ void __launch_bounds__(kWarps * 32, 2) w4_few_up_kernel(const __grid_constant__ FewArgs a) {
-  constexpr int AHEAD = 2, P = Acts<X>::kPlanes;
-  extern __shared__ uint4 acts[];  // [step][word][plane][column][quarter], a piece of zeros, then the scales [step][8]
-  __shared__ float red[kWarps][2][kTile][kFewTokens + 1];
+// The largest integer used, somewhat below P signed bytes 127, 127, ... (8355711 for three: a product with fp32's 24 bits may
+// end a unit above).
+template <int P> constexpr float kMostInt = P == 2 ? 32630.f : 8355000.f;
+
+// Scale of 16 values whose largest magnitude has the pattern `amax`, and its inverse.  Values that are no finite numbers
+// make it NaN; below 2^-100 all count as zeros.  The scale carries the 1/16 of the weights' bytes.
+template <int P>
+__device__ __forceinline__ float int_scale(uint32_t amax, float* inverse) {
+  const float m = __uint_as_float(amax);
+  *inverse = m < 0x1p-100f || amax >= 0x7f800000u ? 0.f : kMostInt<P> / m;
+  return amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : m < 0x1p-100f ? 0.f : m * (1.0f / (16.0f * kMostInt<P>));
+}
+// The bytes of an integer, the highest first.
+template <int P>
+__device__ __forceinline__ void int_bytes(int q, int* digit) {
+#pragma unroll
+  for (int p = P - 1; p > 0; --p) {
+    digit[p] = (int)(signed char)q;
+    q = (q - digit[p]) >> 8;
+  }
+  digit[0] = q;
+}
+// Place of input i of 16 in its 16 bytes: per 8 inputs the even ones, then the odd ones, as a word's nibbles lie.
+__device__ __forceinline__ int byte_place(int i) { return (i & 8) | ((i & 1) << 2) | ((i >> 1) & 3); }
+
+// Sixteen consecutive activations as fp32.
+__device__ __forceinline__ void load16(const float* p, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+    f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+  }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) unpack(__ldg(reinterpret_cast<const uint4*>(p) + i), f + 8 * i, __nv_bfloat16());
+}
+__device__ __forceinline__ void load16(const E4M3* p, float* f) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3)));
+    f[2 * i] = v.x; f[2 * i + 1] = v.y;
+  }
+}
+
+// A lane's activations of a step: its four words' inputs, P bytes each, and their scales (one for two words, with
+// groups of 32 one a word).  Rows in shared memory are padded to whole steps with zeros.
+template <int P, int G>
+struct IntActs {
+  static constexpr int kScales = G == 32 ? 4 : 2;
+  uint32_t q[P][4][2];
+  float s[kScales];
+
+  // bytes, scale: the row's at the lane's first input k of the step (k / 16 pieces from the row's start)
+  __device__ __forceinline__ void load(const unsigned char* bytes, const float* scale, int k) {
+#pragma unroll
+    for (int i = 0; i < kScales; ++i) {
+      const int block = G == 128 ? i : i * (G / 16);  // of one or two words
+      s[i] = scale[block];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const unsigned char* b = bytes + (block * P + p) * 16;
+        if constexpr (G == 32) {
+          const uint2 u = *reinterpret_cast<const uint2*>(b + (k & 8));
+          q[p][i][0] = u.x; q[p][i][1] = u.y;
+        } else {
+          const uint4 u = *reinterpret_cast<const uint4*>(b);
+          q[p][2 * i][0] = u.x; q[p][2 * i][1] = u.y; q[p][2 * i + 1][0] = u.z; q[p][2 * i + 1][1] = u.w;
+        }
+      }
+    }
+  }
+  // Sum over the lane's inputs of the step of one output: w its words, g the groups' scales.
+  __device__ __forceinline__ float dot(const uint32_t* w, const __nv_bfloat16* g) const {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kScales; ++i) {
+      constexpr int WORDS = 4 / kScales;
+      int d[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) d[p] = 0;
+#pragma unroll
+      for (int j = 0; j < WORDS; ++j) {
+        // the signed bytes 16 (nibble - 8): even inputs, odd inputs
+        const int even = (int)(((w[i * WORDS + j] << 4) ^ 0x88888888u) & 0xf0f0f0f0u);
+        const int odd = (int)((w[i * WORDS + j] ^ 0x88888888u) & 0xf0f0f0f0u);
+#pragma unroll
+        for (int p = 0; p < P; ++p) d[p] = __dp4a(odd, (int)q[p][i * WORDS + j][1], __dp4a(even, (int)q[p][i * WORDS + j][0], d[p]));
+      }
+      const float v = P == 2 ? (float)(d[0] * 256 + d[1]) : fmaf((float)(d[0] * 256 + d[1]), 256.f, (float)d[P - 1]);
+      if constexpr (G == 128) sum = i == 0 ? v * s[i] : fmaf(v, s[i], sum);
+      else sum = fmaf(v * s[i], __bfloat162float(g[i]), sum);
+    }
+    return G == 128 ? sum * __bfloat162float(g[0]) : sum;
+  }
+};
+
+// A lane's words and scales of a step, for outputs g and g + 8 of MATS matrices.
+template <int G, int MATS>
+struct IntWeights {
+  uint32_t w[MATS][2][4] = {};
+  __nv_bfloat16 s[MATS][2][kStep / G];
+
+  // q, s: of output g at the lane's first input of the step; q8, s8: to output g + 8; k: that input
+  __device__ __forceinline__ void load(const unsigned char* const* q, const __nv_bfloat16* const* sc, uint32_t q8, uint32_t s8, int k,
+                                       int k0, int K) {
+#pragma unroll
+    for (int i = 0; i < kStep / G; ++i) {
+      const bool in = k + i * G < K;  // K is a multiple of 32: of a lane's G / 4 inputs none or all are inside
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const unsigned char* p = q[m] + r * q8;
+          if (in) {  // beyond K the words keep what they held: the activations there are zeros
+            if constexpr (G == 128) {
+              const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+              w[m][r][0] = u.x; w[m][r][1] = u.y; w[m][r][2] = u.z; w[m][r][3] = u.w;
+            } else if constexpr (G == 64) {
+              const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + 32 * i));
+              w[m][r][2 * i] = u.x; w[m][r][2 * i + 1] = u.y;
+            } else {
+              w[m][r][i] = __ldg(reinterpret_cast<const uint32_t*>(p + 16 * i));
+            }
+          }
+          if (G == 128 || i == 0 || k0 + i * G < K) s[m][r][i] = sc[m][r * s8 + i];
+          else s[m][r][i] = __float2bfloat16_rn(0.f);
+        }
+    }
+  }
+};
+
+// `a` of 32 outputs of the slot's expert for the tokens that chose it: two tiles of outputs, the inputs' steps over four
+// warps each.  One slot a row of topk_idx: the first row of an expert does them all.  ROWS: 1 for one token, else 8.
+template <typename X, int P, int G, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few_up_kernel(const __grid_constant__ FewArgs a) {
+  constexpr int AHEAD = kUpAhead, SPLIT = kWarps / 2;
+  extern __shared__ uint4 acts[];  // bytes [row][8 S][P][16], then scales [row][8 S]
+  __shared__ float red[kWarps][2][kTile][ROWS + (ROWS > 1)];
   __shared__ int token[kFewTokens];
-  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, tile = warp / SPLIT, part = warp % SPLIT;
   launch_dependents();
-  const int rows = a.T * a.k, S = (a.K + kStep - 1) / kStep;
+  const int rows = a.T * a.k, S = (a.K + kStep - 1) / kStep, blocks = S * 8;
   const int e = __ldg(a.topk_idx + blockIdx.y);
   if ((unsigned)e >= (unsigned)a.E) return;  // flagged by the second kernel
-  const LanePlace<G> at(blockIdx.x * kTile, a.K, lane);
-  W4Mat mats[2];
+  const LanePlace<G> at((blockIdx.x * 2 + tile) * kTile, a.K, lane);
+  const unsigned char* q[2];
+  const __nv_bfloat16* sc[2];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    mats[m].q = a.mat[m].q + (size_t)e * a.N * (a.K / 2);
-    mats[m].s = a.mat[m].s + (size_t)e * a.N * ((a.K + G - 1) / G);
+    q[m] = a.mat[m].q + (size_t)e * a.N * (a.K / 2) + at.q + part * (kStep / 2);
+    sc[m] = a.mat[m].s + (size_t)e * a.N * ((a.K + G - 1) / G) + at.s + part * (kStep / G);
   }
-  Weights<G, 2> w[AHEAD];
+  int ahead = part;  // the next step to load
+  IntWeights<G, 2> w[AHEAD];
+  auto load = [&](IntWeights<G, 2>& to) {
+    if (ahead < S) to.load(q, sc, at.q8, at.s8, ahead * kStep + at.k, ahead * kStep, a.K);
+    ahead += SPLIT;
 #pragma unroll
-  for (int d = 0; d < AHEAD; ++d)
-    if (warp + d * kWarps < S) w[d].load(mats, at, a.K, warp + d * kWarps);
-  const unsigned long long mask = rows_of(a.topk_idx, rows, e, lane);
+    for (int m = 0; m < 2; ++m) {
+      q[m] += SPLIT * (kStep / 2);
+      sc[m] += SPLIT * (kStep / G);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d) load(w[d]);
+  unsigned long long mask = rows_of(a.topk_idx, rows, e, lane);
   if (__ffsll(mask) - 1 != (int)blockIdx.y) return;  // an earlier row's block does this expert
   const bool mine = lane < a.T && bits_of(mask, lane < a.T ? lane : 0, a.k) != 0;
   const unsigned chosen = __ballot_sync(0xffffffffu, mine);
   const int n = __popc(chosen);
   if (mine) token[__popc(chosen & ((1u << lane) - 1u))] = lane;  // every warp writes the same
   __syncwarp();
-  const int zeros = S * 4 * P * n * 4;
-  float* scales = reinterpret_cast<float*>(acts + zeros + 1);
-  if (threadIdx.x == 0) acts[zeros] = make_uint4(0, 0, 0, 0);
+  float* scales = reinterpret_cast<float*>(acts + (size_t)n * blocks * P);
   for (int r = 0; r < n; ++r) {
     const X* x = static_cast<const X*>(a.x) + (size_t)token[r] * a.K;
-    for (int i = threadIdx.x; i < S * 16; i += kWarps * 32) {
-      uint32_t b[P][4] = {};
-      if (i * 8 < a.K) Acts<X>::load(x + i * 8, b);
-      int word, quarter;
-      place_of<G>(i % 16, &word, &quarter);
+    for (int i = threadIdx.x; i < blocks; i += kWarps * 32) {
+      float f[16] = {}, inverse;
+      if (i * 16 < a.K) load16(x + i * 16, f);
+      uint32_t amax = 0;
 #pragma unroll
-      for (int p = 0; p < P; ++p)
-        acts[((i / 16 * 4 + word) * P + p) * n * 4 + r * 4 + quarter] = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
+      for (int c = 0; c < 16; ++c) amax = max(amax, __float_as_uint(f[c]) & 0x7fffffffu);
+      float scale = int_scale<P>(amax, &inverse);
+      if constexpr (sizeof(X) == 1) scale *= __ldg(a.x_scale + (size_t)token[r] * S + i / 8);
+      scales[r * blocks + i] = scale;
+      uint32_t word[P][4] = {};
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        int digit[P];
+        int_bytes<P>(__float2int_rn(f[c] * inverse), digit);
+        const int to = byte_place(c);
+#pragma unroll
+        for (int p = 0; p < P; ++p) word[p][to / 4] |= (uint32_t)(digit[p] & 0xff) << (8 * (to % 4));
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) acts[(r * blocks + i) * P + p] = make_uint4(word[p][0], word[p][1], word[p][2], word[p][3]);
     }
-    if (a.x_scale != nullptr)
-      for (int i = threadIdx.x; i < S; i += kWarps * 32) scales[i * 8 + r] = __ldg(a.x_scale + (size_t)token[r] * S + i);
   }
   __syncthreads();
-  // lanes of columns without a row read the piece of zeros
-  const int col = lane / 4, c0 = (lane % 4) * 2;
-  const uint4* from = acts + (col < n ? lane : zeros);
-  const int stride = col < n ? n * 4 : 0;
-  float acc[2][4] = {};
-  for (int s0 = warp; s0 < S; s0 += kWarps * AHEAD) {
+  const unsigned char* bytes = reinterpret_cast<const unsigned char*>(acts) + (part * 8 + at.k / 16) * (16 * P);
+  const float* scale = scales + part * 8 + at.k / 16;
+  float acc[2][2][ROWS] = {};
+  for (int s0 = part; s0 < S; s0 += SPLIT * AHEAD) {
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d) {
-      const int s = s0 + d * kWarps;
-      if (s >= S) break;
-      float x0 = 1.f, x1 = 1.f;
-      if (sizeof(X) == 1) {  // columns beyond n hold whatever is there, and are not read in the end
-        const float2 xs = *reinterpret_cast<const float2*>(scales + s * 8 + c0);
-        x0 = xs.x;
-        x1 = xs.y;
+      if (s0 + d * SPLIT >= S) break;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        if (r >= n) break;
+        IntActs<P, G> x;
+        x.load(bytes + r * blocks * (16 * P), scale + r * blocks, at.k);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int o = 0; o < 2; ++o) acc[m][o][r] += x.dot(w[d].w[m][o], w[d].s[m][o]);
       }
-      const uint4* b = from + s * 4 * P * stride;
-#pragma unroll
-      for (int i = 0; i < kStep / G; ++i)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t f[G / 32][2][4];
-#pragma unroll
-          for (int j = 0; j < G / 32; ++j) unpack_word(w[d].w[m][0][i * (G / 32) + j], w[d].w[m][1][i * (G / 32) + j], f[j]);
-          float part[4];
-          group_product<P, G>(f, [&](int j, int p) { return b[((i * (G / 32) + j) * P + p) * stride]; }, part);
-          const float g0 = __bfloat162float(w[d].s[m][0][i]), g1 = __bfloat162float(w[d].s[m][1][i]);
-          acc[m][0] = fmaf(part[0], sizeof(X) == 1 ? g0 * x0 : g0, acc[m][0]);
-          acc[m][1] = fmaf(part[1], sizeof(X) == 1 ? g0 * x1 : g0, acc[m][1]);
-          acc[m][2] = fmaf(part[2], sizeof(X) == 1 ? g1 * x0 : g1, acc[m][2]);
-          acc[m][3] = fmaf(part[3], sizeof(X) == 1 ? g1 * x1 : g1, acc[m][3]);
-        }
-      if (s + AHEAD * kWarps < S) w[d].load(mats, at, a.K, s + AHEAD * kWarps);
+      bytes += SPLIT * 8 * (16 * P);
+      scale += SPLIT * 8;
+      load(w[d]);
     }
   }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) red[warp][m][lane / 4 + (c / 2) * 8][c0 + c % 2] = acc[m][c];
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        float v = acc[m][o][r];
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        if (lane % 4 == 0) red[warp][m][lane / 4 + o * 8][r] = v;
+      }
   __syncthreads();
-  if (threadIdx.x < kTile * kFewTokens) {
-    const int o = threadIdx.x % kTile, c = threadIdx.x / kTile;
-    if (c < n) {
-      float v[2] = {0.f, 0.f};
+  for (int i = threadIdx.x; i < 2 * kTile * ROWS; i += kWarps * 32) {  // 16 threads a tile's row: whole warps
+    const int o = i % kTile, t = i / kTile % 2, r = i / (2 * kTile);
+    const bool on = r < n;
+    float v[2] = {0.f, 0.f};
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int q = 0; q < kWarps; ++q) v[m] += red[q][m][o][c];
-      __nv_bfloat16 plane[PA];
-      split_planes<PA>(v[0] * sigmoidf_(v[0]) * v[1], plane);
-      const size_t row = (size_t)token[c] * a.k + __ffsll(bits_of(mask, token[c], a.k)) - 1, o1 = paired(blockIdx.x * kTile + o);
+      for (int c = 0; c < SPLIT; ++c) v[m] += red[t * SPLIT + c][m][o][r];
+    const float value = on ? v[0] * sigmoidf_(v[0]) * v[1] : 0.f;
+    uint32_t amax = __float_as_uint(value) & 0x7fffffffu;
 #pragma unroll
-      for (int p = 0; p < PA; ++p) static_cast<__nv_bfloat16*>(a.out)[((size_t)p * rows + row) * a.N + o1] = plane[p];
+    for (int c = 8; c > 0; c >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, c));
+    float inverse;
+    const float sx = int_scale<P>(amax, &inverse);
+    if (on) {
+      const size_t row = (size_t)token[r] * a.k + __ffsll(bits_of(mask, token[r], a.k)) - 1, block = row * (a.N / 16) + blockIdx.x * 2 + t;
+      int digit[P];
+      int_bytes<P>(__float2int_rn(value * inverse), digit);
+#pragma unroll
+      for (int p = 0; p < P; ++p) a.bytes[(block * P + p) * 16 + byte_place(o)] = (unsigned char)digit[p];
+      if (o == 0) a.scales[block] = sx;
     }
   }
 }
 
-// y of 16 outputs for all tokens: the steps of all experts' products, one after another over the warps.  An expert's
-// row is column t of token t, and joins the token's sum with its weight, so the sum over experts stays in registers.
-template <typename T, int PA, int G>
-__global__ void __launch_bounds__(kWarps * 32, 2) w4_few_down_kernel(const __grid_constant__ FewArgs a) {
-  constexpr int AHEAD = PA == 2 ? 4 : 2;  // steps of weights under way; three planes leave room for two
-  __shared__ float red[kWarps][kTile][kFewTokens + 1];
-  __shared__ int expert[kFewRows], row[kFewRows][kFewTokens], idx[kFewRows];
-  __shared__ float weight[kFewRows][kFewTokens];
+// y of 16 outputs for all tokens: the steps of all experts' products over the warps, each token's sum over its experts in
+// registers.
+template <typename T, int P, int G, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kDownBlocks : 2) w4_few_down_kernel(const __grid_constant__ FewArgs a) {
+  constexpr int AHEAD = kDownAhead;
+  extern __shared__ uint4 acts[];  // `a`: bytes [row][8 S][P][16], then scales [row][8 S]
+  __shared__ float red[kWarps][kTile][ROWS + (ROWS > 1)];
+  __shared__ int expert[kFewRows], row[kFewRows][ROWS], idx[kFewRows];
+  __shared__ float weight[kFewRows][ROWS];
   __shared__ unsigned lead[2];
+  __shared__ unsigned short list[kWarps][kFewSteps];
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-  const int rows = a.T * a.k;
+  const int rows = a.T * a.k, S = (a.K + kStep - 1) / kStep, blocks = S * 8;
   // the experts of these tokens, ascending, with each token's row of `a` and weight
   if (threadIdx.x < kFewRows) idx[threadIdx.x] = threadIdx.x < rows ? __ldg(a.topk_idx + threadIdx.x) : -1;
   __syncthreads();
@@ -364,114 +530,104 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_few_down_kernel(const __gri
     if (lane == 0) lead[warp] = ballot;
     asm volatile("bar.sync 1, 64;" ::: "memory");
     if (leads) {
-      const int at = __popcll(below & (lead[0] | (unsigned long long)lead[1] << 32));
-      expert[at] = e;
-      for (int t = 0; t < kFewTokens; ++t) {
+      const int place = __popcll(below & (lead[0] | (unsigned long long)lead[1] << 32));
+      expert[place] = e;
+      for (int t = 0; t < ROWS; ++t) {
         unsigned long long mine = t < a.T ? bits_of(mask, t, a.k) : 0;
-        row[at][t] = mine != 0 ? t * a.k + __ffsll(mine) - 1 : -1;
+        row[place][t] = mine != 0 ? t * a.k + __ffsll(mine) - 1 : -1;
         float sum = 0.f;
         for (; mine != 0; mine &= mine - 1) sum += __ldg(a.topk_w + t * a.k + __ffsll(mine) - 1);
-        weight[at][t] = sum;
+        weight[place][t] = sum;
       }
     }
   }
   __syncthreads();
-  // Warp w takes the steps kb = w - e (mod 8) of expert e, so that a token's sum is the same whatever else is in the batch
-  // (experts that are not its own add zeros), and experts whose steps are no multiple of 8 load the warps evenly.
-  const int S = (a.K + kStep - 1) / kStep, experts = __popc(lead[0]) + __popc(lead[1]);
-  const LanePlace<G> at(blockIdx.x * kTile, a.K, lane);
-  struct Place { int l, kb; };
-  auto enter = [&](Place p) {  // the first step from p on
-    while (p.l < experts && p.kb >= S) {
-      if (++p.l < experts) p.kb = (warp - expert[p.l]) & (kWarps - 1);
+  // Warp w takes the steps kb = w - e (mod 8) of expert e, so that a token's sum is the same whatever else is in the batch,
+  // and experts whose steps are no multiple of 8 load the warps evenly.  Its list: (kb, number of the expert), experts in
+  // order.  At most kFewSteps: the few form's rows x steps are bounded by their shared memory.
+  const int experts = __popc(lead[0]) + __popc(lead[1]);
+  int steps = 0;
+  for (int l0 = 0; l0 < experts; l0 += kWarp) {
+    const int l = l0 + lane, kb0 = l < experts ? (warp - expert[l]) & (kWarps - 1) : S;
+    const int count = kb0 < S ? (S - kb0 + kWarps - 1) / kWarps : 0;
+    int upto = count;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    return p;
-  };
-  auto after = [&](Place p) { return enter(Place{p.l, p.kb + kWarps}); };
-  auto load = [&](Place p, Weights<G, 1>& to) {
-    const W4Mat mat{a.mat[0].q + (size_t)expert[p.l] * a.N * (a.K / 2), a.mat[0].s + (size_t)expert[p.l] * a.N * ((a.K + G - 1) / G)};
-    to.load(&mat, at, a.K, p.kb);
-  };
-  Weights<G, 1> w[AHEAD];
-  Place now = enter(Place{0, experts > 0 ? (warp - expert[0]) & (kWarps - 1) : 0}), ahead = now;
-#pragma unroll
-  for (int d = 0; d < AHEAD; ++d)
-    if (ahead.l < experts) {
-      load(ahead, w[d]);
-      ahead = after(ahead);
-    }
-  wait_dependency();  // `a` is read from here on; the weights above are nobody's output
-  const int col = lane / 4, c0 = (lane % 4) * 2;
-  const size_t plane = (size_t)rows * a.K;
-  // A step's activations, loaded a step ahead.  Columns without a row keep zeros; they are set where the expert changes.
-  uint4 b[2][4][PA];
-  auto fetch = [&](Place p, bool other_expert, uint4 (*to)[PA]) {
-    const int r = row[p.l][col];
-    if (other_expert) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < PA; ++q) to[i][q] = make_uint4(0, 0, 0, 0);
-    }
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + (size_t)(r < 0 ? 0 : r) * a.K + p.kb * kStep + at.k;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = i / (G / 32) * G + i % (G / 32) * 8;
-      if (r >= 0 && p.kb * kStep + at.k + k < a.K) {
-#pragma unroll
-        for (int q = 0; q < PA; ++q) to[i][q] = *reinterpret_cast<const uint4*>(x + q * plane + k);
-      } else if (r >= 0) {
-#pragma unroll
-        for (int q = 0; q < PA; ++q) to[i][q] = make_uint4(0, 0, 0, 0);
-      }
-    }
-  };
-  float acc[4] = {};
-  int filled[2] = {-1, -1};  // the expert that each buffer's zeros are of
-  if (now.l < experts) {
-    fetch(now, true, b[0]);
-    filled[0] = now.l;
+    for (int i = 0; i < count; ++i) list[warp][steps + upto - count + i] = (unsigned short)(l | (kb0 + i * kWarps) << 6);
+    steps += __shfl_sync(0xffffffffu, upto, kWarp - 1);
   }
-  while (now.l < experts) {
+  __syncwarp();
+  const LanePlace<G> at(blockIdx.x * kTile, a.K, lane);
+  int ahead = 0;
+  IntWeights<G, 1> w[AHEAD];
+  auto load = [&](IntWeights<G, 1>& to) {
+    if (ahead < steps) {
+      const int l = list[warp][ahead] & 63, kb = list[warp][ahead] >> 6;
+      const unsigned char* q = a.mat[0].q + (size_t)expert[l] * a.N * (a.K / 2) + at.q + kb * (kStep / 2);
+      const __nv_bfloat16* sc = a.mat[0].s + (size_t)expert[l] * a.N * ((a.K + G - 1) / G) + at.s + kb * (kStep / G);
+      to.load(&q, &sc, at.q8, at.s8, kb * kStep + at.k, kb * kStep, a.K);
+    }
+    ++ahead;
+  };
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d) load(w[d]);
+  float* scales = reinterpret_cast<float*>(acts + (size_t)rows * blocks * P);
+  if (a.K % kStep != 0) {  // the padding of a row's last step
+    const int inside = a.K / 16, pad = blocks - inside;
+    for (int i = threadIdx.x; i < rows * pad; i += kWarps * 32) {
+      const int to = i / pad * blocks + inside + i % pad;
+      scales[to] = 0.f;
+#pragma unroll
+      for (int p = 0; p < P; ++p) acts[to * P + p] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  wait_dependency();  // `a` is read from here on; the weights above are nobody's output
+  for (int r = 0; r < rows; ++r) {
+    const uint4* from = reinterpret_cast<const uint4*>(a.bytes) + (size_t)r * (a.K / 16) * P;
+    for (int i = threadIdx.x; i < a.K / 16 * P; i += kWarps * 32) ptx::cp_async_16(ptx::smem_u32(acts + r * blocks * P + i), from + i, 16);
+    for (int i = threadIdx.x; i < a.K / 16; i += kWarps * 32) scales[r * blocks + i] = a.scales[(size_t)r * (a.K / 16) + i];
+  }
+  ptx::cp_async_commit();
+  ptx::cp_async_wait<0>();
+  __syncthreads();
+  float acc[2][ROWS] = {};
+  for (int i0 = 0; i0 < steps; i0 += AHEAD) {
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d) {
-      if (now.l >= experts) break;
-      const Place next = after(now);
-      if (next.l < experts) {
-        fetch(next, next.l != filled[(d + 1) & 1], b[(d + 1) & 1]);
-        filled[(d + 1) & 1] = next.l;
-      }
-      const float x0 = weight[now.l][c0], x1 = weight[now.l][c0 + 1];
+      if (i0 + d >= steps) break;
+      const int l = list[warp][i0 + d] & 63, block = (list[warp][i0 + d] >> 6) * 8 + at.k / 16;
 #pragma unroll
-      for (int i = 0; i < kStep / G; ++i) {
-        uint32_t f[G / 32][2][4];
+      for (int t = 0; t < ROWS; ++t) {
+        const int r = row[l][t];
+        if (ROWS > 1 && r < 0) continue;
+        IntActs<P, G> x;
+        x.load(reinterpret_cast<const unsigned char*>(acts) + (r * blocks + block) * (16 * P), scales + r * blocks + block, at.k);
 #pragma unroll
-        for (int j = 0; j < G / 32; ++j) unpack_word(w[d].w[0][0][i * (G / 32) + j], w[d].w[0][1][i * (G / 32) + j], f[j]);
-        float part[4];
-        group_product<PA, G>(f, [&](int j, int p) { return b[d & 1][i * (G / 32) + j][p]; }, part);
-        const float g0 = __bfloat162float(w[d].s[0][0][i]), g1 = __bfloat162float(w[d].s[0][1][i]);
-        acc[0] = fmaf(part[0], g0 * x0, acc[0]);
-        acc[1] = fmaf(part[1], g0 * x1, acc[1]);
-        acc[2] = fmaf(part[2], g1 * x0, acc[2]);
-        acc[3] = fmaf(part[3], g1 * x1, acc[3]);
+        for (int o = 0; o < 2; ++o) acc[o][t] = fmaf(x.dot(w[d].w[0][o], w[d].s[0][o]), weight[l][t], acc[o][t]);
       }
-      if (ahead.l < experts) {
-        load(ahead, w[d]);
-        ahead = after(ahead);
-      }
-      now = next;
+      load(w[d]);
     }
   }
 #pragma unroll
-  for (int c = 0; c < 4; ++c) red[warp][lane / 4 + (c / 2) * 8][c0 + c % 2] = acc[c];
+  for (int o = 0; o < 2; ++o)
+#pragma unroll
+    for (int t = 0; t < ROWS; ++t) {
+      float v = acc[o][t];
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      v += __shfl_xor_sync(0xffffffffu, v, 2);
+      if (lane % 4 == 0) red[warp][lane / 4 + o * 8][t] = v;
+    }
   __syncthreads();
-  if (threadIdx.x < kTile * kFewTokens) {
+  if (threadIdx.x < kTile * ROWS) {
     const int o = threadIdx.x % kTile, t = threadIdx.x / kTile;
     if (t < a.T) {
       float v = 0.f;
 #pragma unroll
       for (int q = 0; q < kWarps; ++q) v += red[q][o][t];
-      static_cast<T*>(a.out)[(size_t)t * a.N + blockIdx.x * kTile + o] = from_f<T>(v);
+      static_cast<T*>(a.y)[(size_t)t * a.N + blockIdx.x * kTile + o] = from_f<T>(v);
     }
   }
 }
@@ -731,13 +887,13 @@ void launch_early(void (*kernel)(A), dim3 grid, int threads, size_t bytes, cudaS
   count_launch(st);
 }
 
-template <typename T> constexpr int kActPlanes = sizeof(T) == 2 ? 2 : 3;  // planes of `a`
+template <typename T> constexpr int kActPlanes = sizeof(T) == 2 ? 2 : 3;  // bf16 planes of `a`, many form
+template <typename T> constexpr int kIntPlanes = sizeof(T) == 2 ? 2 : 3;  // bytes of an activation, few form
 
-// Shared memory of the few form's first kernel with T rows.
-template <typename X>
-size_t few_bytes(int T, int K) {
-  const size_t S = (K + kStep - 1) / kStep;
-  return (S * 16 * Acts<X>::kPlanes * T + 1) * 16 + S * 8 * sizeof(float);
+// Shared memory of `rows` rows of K activations in the few form.
+template <typename T>
+size_t few_bytes(int rows, int K) {
+  return (size_t)rows * ((K + kStep - 1) / kStep) * 8 * (16 * kIntPlanes<T> + sizeof(float));
 }
 
 template <typename K>
@@ -750,19 +906,22 @@ void allow_shared(K kernel, int bytes, bool* ready) {  // per device: the attrib
   }
 }
 
-template <typename X, typename T, int G>
+template <typename X, typename T, int G, int ROWS>
 void few(const W4Ffn& p, cudaStream_t st) {
-  constexpr int PA = kActPlanes<T>;
+  constexpr int P = kIntPlanes<T>;
+  unsigned char* bytes = static_cast<unsigned char*>(p.a);
+  float* scales = reinterpret_cast<float*>(bytes + (size_t)p.T * p.k * p.f * P);
   const FewArgs up{p.x, p.x_scale, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.h, p.f,
                    {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
-                    {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, p.a, p.status};
-  static bool ready[64] = {};
-  allow_shared(w4_few_up_kernel<X, PA, G>, kFewBytes, ready);
-  w4_few_up_kernel<X, PA, G><<<dim3(p.f / kTile, p.T * p.k), kWarps * 32, few_bytes<X>(p.T, p.h), st>>>(up);
+                    {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, bytes, scales, nullptr, p.status};
+  static bool ready[2][64] = {};
+  allow_shared(w4_few_up_kernel<X, P, G, ROWS>, kFewBytes, ready[0]);
+  w4_few_up_kernel<X, P, G, ROWS><<<dim3(p.f / (2 * kTile), p.T * p.k), kWarps * 32, few_bytes<T>(p.T, p.h), st>>>(up);
   count_launch(st);
-  const FewArgs down{p.a, nullptr, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.f, p.h,
-                     {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.y, p.status};
-  launch_early(w4_few_down_kernel<T, PA, G>, dim3(p.h / kTile), kWarps * 32, 0, st, down);
+  const FewArgs down{nullptr, nullptr, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.f, p.h,
+                     {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, bytes, scales, p.y, p.status};
+  allow_shared(w4_few_down_kernel<T, P, G, ROWS>, kFewBytes, ready[1]);
+  launch_early(w4_few_down_kernel<T, P, G, ROWS>, dim3(p.h / kTile), kWarps * 32, few_bytes<T>(p.T * p.k, p.f), st, down);
 }
 
 template <int P, int PA, int G, bool GATEUP, bool SCALED>
@@ -802,12 +961,20 @@ void many(const W4Ffn& p, cudaStream_t st) {
   count_launch(st);
 }
 
+template <typename X, typename T, int G>
+void run_group(const W4Ffn& p, cudaStream_t st) {
+  const bool is_few = p.T <= kFewTokens && p.T * p.k <= kFewRows && few_bytes<T>(p.T, p.h) <= (size_t)kFewBytes &&
+                      few_bytes<T>(p.T * p.k, p.f) <= (size_t)kFewBytes;
+  if (!is_few) many<X, T, G>(p, st);
+  else if (p.T == 1) few<X, T, G, 1>(p, st);
+  else few<X, T, G, kFewTokens>(p, st);
+}
+
 template <typename X, typename T>
 void run(const W4Ffn& p, cudaStream_t st) {
-  const bool is_few = p.T <= kFewTokens && p.T * p.k <= kFewRows && few_bytes<X>(p.T, p.h) <= (size_t)kFewBytes;
-  if (p.group == 128) is_few ? few<X, T, 128>(p, st) : many<X, T, 128>(p, st);
-  else if (p.group == 64) is_few ? few<X, T, 64>(p, st) : many<X, T, 64>(p, st);
-  else is_few ? few<X, T, 32>(p, st) : many<X, T, 32>(p, st);
+  if (p.group == 128) run_group<X, T, 128>(p, st);
+  else if (p.group == 64) run_group<X, T, 64>(p, st);
+  else run_group<X, T, 32>(p, st);
 }
 
 }  // namespace
