@@ -183,7 +183,7 @@ size_t moe_workspace_size(int op, int T, int h, int E, int k, int f, int dtype) 
     case MOE_OP_ADD_RMSNORM_BWD:
       return hdr + round256((size_t)kNormMaxParts * std::max(h, 0) * sizeof(float));
     case MOE_OP_EXPERT_FFN_W4:
-      return hdr + w4_scratch(dtype, std::max(T, 0), std::max(k, 0), std::max(h, 0), std::max(f, 0), nullptr);
+      return hdr + w4_scratch(dtype, std::max(T, 0), std::max(k, 0), std::max(h, 0), std::max(E, 1), std::max(f, 0), nullptr);
     case MOE_OP_ALL: {
       size_t m = 0;
       for (int o = 0; o < MOE_OP_ALL; ++o) m = std::max(m, moe_workspace_size(o, T, h, E, k, f, dtype));
@@ -684,9 +684,9 @@ int moe_expert_ffn_w4(const void* x, const float* x_scale, const int32_t* topk_i
   REQUIRE_PTR(W3s); REQUIRE_PTR(W2q); REQUIRE_PTR(W2s); REQUIRE_PTR(y);
   char* base = static_cast<char*>(ws) + sizeof(WsHeader);
   W4Scratch at;
-  w4_scratch(dtype, T, k, h, f, &at);
+  w4_scratch(dtype, T, k, h, E, f, &at);
   const W4Ffn p{x, x_scale, topk_idx, topk_w, W1q, W1s, W3q, W3s, W2q, W2s, T, k, E, h, f, group, y, base + at.a,
-                reinterpret_cast<float*>(base + at.rows), base + at.x_planes, status_of(ws)};
+                reinterpret_cast<float*>(base + at.rows), base + at.x_planes, base + at.plan, status_of(ws)};
   launch_expert_ffn_w4(dtype, p, (cudaStream_t)stream);
   return check_launch("moe_expert_ffn_w4");
 }

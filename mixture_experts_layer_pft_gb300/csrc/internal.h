@@ -129,11 +129,11 @@ constexpr int kAdamwMaxTensors = 384;  // of one launch
 void launch_adamw(const AdamwTensor* t, int n, int first_tensor, const AdamwScalars& c, cudaStream_t st);
 
 // w4.cu -- routed experts over 4-bit weights.  Scratch: a's bf16 planes ([2 or 3][T*k, f]), the experts' output rows
-// ([T*k, h] fp32) and x's planes ([1 or 3][T, h]); w4_scratch: its bytes, and the parts' offsets.
+// ([T*k, h] fp32), x's planes ([1 or 3][T, h]) and the rows by expert; w4_scratch: its bytes, and the parts' offsets.
 struct W4Scratch {
-  size_t a, rows, x_planes;
+  size_t a, rows, x_planes, plan;
 };
-size_t w4_scratch(int dtype, long long T, long long k, int h, int f, W4Scratch* at);
+size_t w4_scratch(int dtype, long long T, long long k, int h, int E, int f, W4Scratch* at);
 struct W4Ffn {
   const void* x;
   const float* x_scale;  // e4m3 activations only
@@ -145,6 +145,7 @@ struct W4Ffn {
   void* a;
   float* rows;
   void* x_planes;
+  void* plan;
   int* status;
 };
 void launch_expert_ffn_w4(int dtype, const W4Ffn& p, cudaStream_t st);

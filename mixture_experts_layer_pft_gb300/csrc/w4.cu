@@ -17,8 +17,8 @@
 //
 // Two forms.  Up to 8 tokens and 64 rows, as far as their activations fit in shared memory ("few"): two launches; token t is column t of every product, warps split the
 // inputs, and the second kernel adds its outputs over all experts in registers, so no row is written but `a`.  Above
-// ("many"): an expert's rows in passes of 32 through shared memory, warps side by side over 64 outputs and two halves of
-// the inputs, experts' output rows to scratch, and a combine.
+// ("many"): an expert's rows in units of 32 (fp32: 16) through shared memory, warps side by side over 64 outputs and two
+// halves of the inputs, experts' output rows to scratch, and a combine.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -33,9 +33,10 @@ constexpr int kWarps = 8;
 constexpr int kTile = 16;       // outputs of a warp
 constexpr int kStep = 128;      // inputs of a warp's step
 constexpr int kFewTokens = 8, kFewRows = 64;
-constexpr int kPass = 32;       // rows of one pass of the many form
-constexpr int kTilesN = kPass / 8;
-constexpr int kManyTiles = 4;   // warps side by side over the outputs, many form
+template <int P> constexpr int kPass = P == 3 ? 16 : 32;  // rows of a unit of the many form, activations in P planes
+// Warps side by side over the outputs, many form (64 tokens of the Medium layer, up / down: 4 / 8 236 us, 4 / 4 273, 8 / 8
+// 229; 13 fp32 ones of the long-sequence layer, whose items are few: 84, 68 and 89).
+template <int P, bool GATEUP> constexpr int kWide = GATEUP || P == 3 ? 4 : 8;
 constexpr int kStages = 3;      // turns of activations in shared memory, many form
 constexpr int kFewBytes = 100 * 1024;  // shared memory for the few form's activations
 constexpr int kFewSteps = 128;         // of a warp: kFewBytes / (128 inputs x 2.25 bytes) / 8, and one more an expert
@@ -55,6 +56,13 @@ __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16_first(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {  // c = a b
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Nibbles i and i + 4 of w as two bf16: 128 + nibble has the nibble as its last mantissa bits.
@@ -142,56 +150,20 @@ struct LanePlace {
   }
 };
 
-// A step's words and scales of MATS matrices' outputs g and g + 8.  Beyond K the words keep what they held: the activations
-// there are zeros, and any nibble is a finite number.
-template <int G, int MATS>
-struct Weights {
-  uint32_t w[MATS][2][4] = {};
-  __nv_bfloat16 s[MATS][2][kStep / G];
-
-  __device__ __forceinline__ void load(const W4Mat* mats, const LanePlace<G>& at, int K, int step) {
-#pragma unroll
-    for (int m = 0; m < MATS; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const unsigned char* q = mats[m].q + (at.q + r * at.q8 + (uint32_t)step * (kStep / 2));
-        const __nv_bfloat16* sc = mats[m].s + (at.s + r * at.s8 + (uint32_t)step * (kStep / G));
-        uint32_t* to = w[m][r];
-#pragma unroll
-        for (int i = 0; i < kStep / G; ++i) {
-          const int k = step * kStep + i * G;
-          if (k + at.k < K) {  // K is a multiple of 32: of a lane's G / 4 inputs none or all are inside
-            if constexpr (G == 128) {
-              const uint4 u = __ldg(reinterpret_cast<const uint4*>(q));
-              to[0] = u.x; to[1] = u.y; to[2] = u.z; to[3] = u.w;
-            } else if constexpr (G == 64) {
-              const uint2 u = __ldg(reinterpret_cast<const uint2*>(q + 32 * i));
-              to[2 * i] = u.x; to[2 * i + 1] = u.y;
-            } else {
-              to[i] = __ldg(reinterpret_cast<const uint32_t*>(q + 16 * i));
-            }
-          }
-          if (G == 128 || i == 0 || k < K) s[m][r][i] = sc[i];
-          else s[m][r][i] = __float2bfloat16_rn(0.f);
-        }
-      }
-  }
-};
-
 // A group's words (their A operands f) with one column tile of activations, all planes.  One or two planes: one chain of
 // sums a group.  Three (fp32): the small planes in a chain of their own, as the tensor core's sums round towards zero.
 template <int P, int G, typename LOAD>
 __device__ __forceinline__ void group_product(const uint32_t (*f)[2][4], LOAD load, float part[4]) {
-  float low[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int c = 0; c < 4; ++c) part[c] = 0.f;
+  float low[4];
 #pragma unroll
   for (int j = 0; j < G / 32; ++j)
 #pragma unroll
     for (int p = P - 1; p >= 0; --p) {
       const uint4 u = load(j, p);
-      float* to = P == 3 && p > 0 ? low : part;
-      mma_bf16(to, f[j][0], u.x, u.y);
+      const bool apart = P == 3 && p > 0;
+      float* to = apart ? low : part;
+      if (j == 0 && (apart ? p == P - 1 : P == 3 || p == P - 1)) mma_bf16_first(to, f[j][0], u.x, u.y);
+      else mma_bf16(to, f[j][0], u.x, u.y);
       mma_bf16(to, f[j][1], u.z, u.w);
     }
   if constexpr (P == 3) {
@@ -634,180 +606,243 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kDownBlocks : 2) w4_f
 
 // ------------------------------------------------------------------------------------ many rows
 
-// x [T, K] to paired bf16 planes [P][T][K].
+// What the products work through: units of an expert and up to `pass` of its rows, and the rows by expert.
+struct ManyPlan {
+  int units, pad[3];
+  int unit[1];  // units x (expert, first place in the rows' list, rows), then the list
+};
+__host__ __device__ __forceinline__ int most_units(int rows, int E, int pass) {  // an expert's last unit may be short
+  return (rows < E ? rows : E) + rows / pass;
+}
+
+// x [T, K] to paired bf16 planes [P][T][K]; block 0 makes the plan.  The place of a row in its expert's part of the list
+// is whichever its atomic gives it: a row is a column of its own in every product, and no result depends on which.
 template <typename X>
-__global__ void __launch_bounds__(256) w4_planes_kernel(const X* __restrict__ x, long long eights, __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x, long long eights, __nv_bfloat16* __restrict__ out,
+                                                         const int* __restrict__ topk_idx, int rows, int E, int pass, ManyPlan* plan) {
   constexpr int P = Acts<X>::kPlanes;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   launch_dependents();
-  if (i >= eights) return;
-  uint32_t b[P][4];
-  Acts<X>::load(x + i * 8, b);
+  if (blockIdx.x > 0) {
+    const long long i = (long long)(blockIdx.x - 1) * 256 + threadIdx.x;
+    if (i >= eights) return;
+    uint32_t b[P][4];
+    Acts<X>::load(x + i * 8, b);
 #pragma unroll
-  for (int p = 0; p < P; ++p) reinterpret_cast<uint4*>(out)[p * eights + i] = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
+    for (int p = 0; p < P; ++p) reinterpret_cast<uint4*>(out)[p * eights + i] = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
+    return;
+  }
+  __shared__ int count[1024], start[1024], total[2];
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  for (int e = threadIdx.x; e < E; e += 256) count[e] = 0;
+  __syncthreads();
+  for (int r = threadIdx.x; r < rows; r += 256) {
+    const int e = __ldg(topk_idx + r);
+    if ((unsigned)e < (unsigned)E) atomicAdd(&count[e], 1);  // others are flagged by the combine
+  }
+  __syncthreads();
+  if (warp == 0) {  // rows and units before each expert
+    int before = 0, units = 0;
+    for (int e0 = 0; e0 < E; e0 += kWarp) {
+      const int e = e0 + lane, c = e < E ? count[e] : 0, u = (c + pass - 1) / pass;
+      int cs = c, us = u;
+#pragma unroll
+      for (int o = 1; o < kWarp; o <<= 1) {
+        const int cv = __shfl_up_sync(0xffffffffu, cs, o), uv = __shfl_up_sync(0xffffffffu, us, o);
+        if (lane >= o) { cs += cv; us += uv; }
+      }
+      if (e < E) {
+        start[e] = before + cs - c;
+        for (int i = 0; i < u; ++i) {
+          int* to = plan->unit + 3 * (units + us - u + i);
+          to[0] = e;
+          to[1] = before + cs - c + i * pass;
+          to[2] = min(c - i * pass, pass);
+        }
+      }
+      before += __shfl_sync(0xffffffffu, cs, kWarp - 1);
+      units += __shfl_sync(0xffffffffu, us, kWarp - 1);
+    }
+    if (lane == 0) plan->units = units;
+  }
+  __syncthreads();
+  int* list = plan->unit + 3 * most_units(rows, E, pass);
+  for (int r = threadIdx.x; r < rows; r += 256) {
+    const int e = __ldg(topk_idx + r);
+    if ((unsigned)e < (unsigned)E) list[atomicAdd(&start[e], 1)] = r;
+  }
 }
 
 struct ManyArgs {
   const __nv_bfloat16* x;  // paired planes [P][xrows][K]
   const float* x_scale;
-  const int* topk_idx;
+  const ManyPlan* plan;
   int rows, k, xrows, E, K, N;  // row r of topk_idx reads x's row r / k (gate/up) or r (down: k = 1)
   W4Mat mat[2];
   void* out;               // gate/up: a's planes [PA][rows][N]; down: [rows, N] fp32
 };
 
-// Rows number lo .. lo + 31 of expert e, ascending, into list; returns how many there are (the block's 256 threads).
-__device__ __forceinline__ int find_rows(const int* __restrict__ topk_idx, int rows, int e, int lo, int* list, int* counts) {
-  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-  int n = 0;
-  for (int pos = 0; pos < rows && n < lo + kPass; pos += kWarps * kWarp) {
-    const int r = pos + threadIdx.x;
-    const bool hit = r < rows && __ldg(topk_idx + r) == e;
-    const unsigned ballot = __ballot_sync(0xffffffffu, hit);
-    __syncthreads();
-    if (lane == 0) counts[warp] = __popc(ballot);
-    __syncthreads();
-    int at = n + __popc(ballot & ((1u << lane) - 1u)) - lo;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) at += counts[i];
-      n += counts[i];
-    }
-    if (hit && at >= 0 && at < kPass) list[at] = r;
-  }
-  __syncthreads();
-  return min(max(n - lo, 0), kPass);
-}
-
-// A block: 64 outputs of the slot's expert, every gridDim.z-th pass of 32 of its rows.  Warps 0-3 take the even steps of 16
-// outputs each, warps 4-7 the odd ones; a turn of the loop is a step of each.
-template <int P, int PA, int G, bool GATEUP, bool SCALED>
-__global__ void __launch_bounds__(kWarps * 32, P == 3 ? 1 : 2) w4_many_kernel(const __grid_constant__ ManyArgs a) {
-  constexpr int MATS = GATEUP ? 2 : 1;
-  constexpr int STEP = kTilesN * 4 * 32 * P;  // 16-byte pieces of a step: [row tile][word][plane][lane]
-  extern __shared__ uint4 stage[];            // [stage][half][STEP]
-  __shared__ int list[kPass], counts[kWarps];
-  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, half = warp / kManyTiles;
+// Blocks take turns at the items, each WIDE tiles of outputs (one a warp) of a unit; with 4 tiles, warps 0-3 take the even
+// steps and 4-7 the odd ones.  A turn of the loop is a step of each.
+template <int P, int PA, int G, bool GATEUP, bool SCALED, int WIDE>
+__global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_constant__ ManyArgs a) {
+  constexpr int MATS = GATEUP ? 2 : 1, TILES = kPass<P> / 8, VALUES = MATS * TILES * 4, SPLIT = kWarps / WIDE;
+  constexpr int STEP = TILES * 4 * 32 * P;  // 16-byte pieces of a step: [row tile][word][plane][lane]
+  extern __shared__ uint4 stage[];          // [stage][step of the turn][STEP]
+  __shared__ int list[kPass<P>], source[kPass<P>];
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, part = warp / WIDE;
   launch_dependents();
   wait_dependency();
-  const bool by_row = a.rows <= a.E;  // one slot a row (the first row of an expert does them all), or a slot an expert
-  const int e = by_row ? __ldg(a.topk_idx + blockIdx.y) : (int)blockIdx.y;
-  if ((unsigned)e >= (unsigned)a.E) return;  // flagged by the combine
-  if (by_row) {
-    bool earlier = false;
-    for (int r = threadIdx.x; r < (int)blockIdx.y; r += kWarps * kWarp) earlier |= __ldg(a.topk_idx + r) == e;
-    if (__syncthreads_or(earlier)) return;
-  }
-  const int out0 = (blockIdx.x * kManyTiles + warp % kManyTiles) * kTile;
-  const bool live = out0 < a.N;
-  const LanePlace<G> at(live ? out0 : 0, a.K, lane);
-  W4Mat mats[MATS];
+  const int across = (a.N + WIDE * kTile - 1) / (WIDE * kTile), items = a.plan->units * across;
+  const int S = (a.K + kStep - 1) / kStep, turns = (S + SPLIT - 1) / SPLIT;
+  const int* rows_by_expert = a.plan->unit + 3 * most_units(a.rows, a.E, kPass<P>);
+  // an item's expert, number of rows and, in thread i, its i-th row: read an item ahead
+  int e = 0, n = 0, r = 0;
+  auto look = [&](int item) {
+    if (item >= items) return;
+    const int* unit = a.plan->unit + 3 * (item / across);
+    e = unit[0];
+    n = unit[2];
+    r = threadIdx.x < n ? rows_by_expert[unit[1] + threadIdx.x] : 0;
+  };
+  look(blockIdx.x);
+  const LanePlace<G> lanes(0, a.K, lane);  // strides, and this lane's place in the first tile
+  const int c = threadIdx.x % (16 * SPLIT), r0 = threadIdx.x / (16 * SPLIT);  // this thread's piece of a turn's activations
+  constexpr int ROWS_FILL = kWarps * 32 / (16 * SPLIT), FILLS = kPass<P> / ROWS_FILL;
+  int word, quarter;
+  place_of<G>(c % 16, &word, &quarter);
+  const int c0 = (lane % 4) * 2;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    __syncthreads();  // the last item's list and stages have been read
+    if (threadIdx.x < n) {
+      list[threadIdx.x] = r;
+      source[threadIdx.x] = r / a.k;
+    }
+    const int out0 = (item % across * WIDE + warp % WIDE) * kTile, rows = n, tiles = (n + 7) / 8;
+    const bool live = out0 < a.N;
+    const unsigned char* q[MATS];
+    const __nv_bfloat16* sc[MATS];
 #pragma unroll
-  for (int m = 0; m < MATS; ++m) {
-    mats[m].q = a.mat[m].q + (size_t)e * a.N * (a.K / 2);
-    mats[m].s = a.mat[m].s + (size_t)e * a.N * ((a.K + G - 1) / G);
-  }
-  const int S = (a.K + kStep - 1) / kStep, turns = (S + 1) / 2;
-  for (int lo = blockIdx.z * kPass;; lo += gridDim.z * kPass) {
-    const int n = find_rows(a.topk_idx, a.rows, e, lo, list, counts);
-    if (n == 0) return;
-    const int tiles = (n + 7) / 8;
-    auto source = [&](int i) { return GATEUP ? list[i] / a.k : list[i]; };
+    for (int m = 0; m < MATS; ++m) {
+      q[m] = a.mat[m].q + ((size_t)e * a.N + (live ? out0 : 0)) * (a.K / 2) + lanes.q + part * (kStep / 2);
+      sc[m] = a.mat[m].s + ((size_t)e * a.N + (live ? out0 : 0)) * ((a.K + G - 1) / G) + lanes.s + part * (kStep / G);
+    }
+    IntWeights<G, MATS> next;
+    int k0 = part * kStep;  // of the weights to load next
+    auto load = [&] {
+      if (k0 < a.K) next.load(q, sc, lanes.q8, lanes.s8, k0 + lanes.k, k0, a.K);
+      k0 += SPLIT * kStep;
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) {
+        q[m] += SPLIT * (kStep / 2);
+        sc[m] += SPLIT * (kStep / G);
+      }
+    };
+    load();
+    __syncthreads();
+    look(item + gridDim.x);
     // a turn's activations: piece (row, eight) of plane p goes where lane (row % 8, quarter) reads it
-    auto fill = [&](int turn) {
-      const uint32_t to = ptx::smem_u32(stage + turn % kStages * 2 * STEP);
-      for (int i = threadIdx.x; i < tiles * 8 * 32; i += kWarps * 32) {
-        const int r = i / 32, c = i % 32, k = turn * 2 * kStep + c * 8;
-        int word, quarter;
-        place_of<G>(c % 16, &word, &quarter);
-        const bool in = r < n && k < a.K;
-        const __nv_bfloat16* from = a.x + (in ? (size_t)source(r) * a.K + k : 0);
+    const __nv_bfloat16* from[FILLS];
+#pragma unroll
+    for (int i = 0; i < FILLS; ++i)
+      from[i] = r0 + i * ROWS_FILL < rows ? a.x + (size_t)source[r0 + i * ROWS_FILL] * a.K + c * 8 : nullptr;
+    auto fill = [&](int turn, int slot) {
+      const uint32_t to = ptx::smem_u32(stage + (slot * SPLIT + c / 16) * STEP);
+      const int k = turn * SPLIT * kStep;
+#pragma unroll
+      for (int i = 0; i < FILLS; ++i) {
+        const int row = r0 + i * ROWS_FILL;
+        if (row >= tiles * 8) break;
+        const bool in = from[i] != nullptr && k + c * 8 < a.K;
+        const __nv_bfloat16* x = in ? from[i] + k : a.x;
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          ptx::cp_async_16(to + (c / 16 * STEP + ((r / 8 * 4 + word) * P + p) * 32 + r % 8 * 4 + quarter) * 16,
-                           from + (size_t)p * a.xrows * a.K, in ? 16u : 0u);
+          ptx::cp_async_16(to + (((row / 8 * 4 + word) * P + p) * 32 + row % 8 * 4 + quarter) * 16, x + (size_t)p * a.xrows * a.K,
+                           in ? 16u : 0u);
       }
     };
 #pragma unroll
     for (int t = 0; t < kStages - 1; ++t) {
-      if (t < turns) fill(t);
+      if (t < turns) fill(t, t);
       ptx::cp_async_commit();
     }
-    Weights<G, MATS> next;
-    if (half < S) next.load(mats, at, a.K, half);
-    const int c0 = (lane % 4) * 2;
-    float acc[MATS][kTilesN][4];
+    float acc[MATS][TILES][4];
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
-      for (int t = 0; t < kTilesN; ++t)
+      for (int t = 0; t < TILES; ++t)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][t][c] = 0.f;
+        for (int v = 0; v < 4; ++v) acc[m][t][v] = 0.f;
+    int slot = 0;
     for (int turn = 0; turn < turns; ++turn) {
       ptx::cp_async_wait<kStages - 2>();
       __syncthreads();  // the turn's activations are there, and the stage before it has been read by all
-      if (turn + kStages - 1 < turns) fill(turn + kStages - 1);
+      if (turn + kStages - 1 < turns) fill(turn + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
       ptx::cp_async_commit();
-      const int s = turn * 2 + half;
-      const Weights<G, MATS> w = next;
-      if (s + 2 < S) next.load(mats, at, a.K, s + 2);
-      if (s >= S) continue;
-      const uint4* b = stage + (turn % kStages * 2 + half) * STEP + lane;
+      const IntWeights<G, MATS> w = next;
+      load();
+      const int s = turn * SPLIT + part;
+      if (s < S) {
+        const uint4* b = stage + (slot * SPLIT + part) * STEP + lane;
 #pragma unroll
-      for (int m = 0; m < MATS; ++m)
+        for (int m = 0; m < MATS; ++m)
 #pragma unroll
-        for (int i = 0; i < kStep / G; ++i) {
-          uint32_t f[G / 32][2][4];
+          for (int i = 0; i < kStep / G; ++i) {
+            uint32_t f[G / 32][2][4];
 #pragma unroll
-          for (int j = 0; j < G / 32; ++j) unpack_word(w.w[m][0][i * (G / 32) + j], w.w[m][1][i * (G / 32) + j], f[j]);
-          const float g0 = __bfloat162float(w.s[m][0][i]), g1 = __bfloat162float(w.s[m][1][i]);
+            for (int j = 0; j < G / 32; ++j) unpack_word(w.w[m][0][i * (G / 32) + j], w.w[m][1][i * (G / 32) + j], f[j]);
+            const float g0 = __bfloat162float(w.s[m][0][i]), g1 = __bfloat162float(w.s[m][1][i]);
 #pragma unroll
-          for (int t = 0; t < kTilesN; ++t) {
-            if (t >= tiles) break;
-            float part[4];
-            group_product<P, G>(f, [&](int j, int p) { return b[((t * 4 + i * (G / 32) + j) * P + p) * 32]; }, part);
-            float x0 = 1.f, x1 = 1.f;
-            if constexpr (SCALED) {
-              x0 = t * 8 + c0 < n ? __ldg(a.x_scale + (size_t)source(t * 8 + c0) * S + s) : 0.f;
-              x1 = t * 8 + c0 + 1 < n ? __ldg(a.x_scale + (size_t)source(t * 8 + c0 + 1) * S + s) : 0.f;
+            for (int t = 0; t < TILES; ++t) {
+              if (t >= tiles) break;
+              float part4[4];
+              group_product<P, G>(f, [&](int j, int p) { return b[((t * 4 + i * (G / 32) + j) * P + p) * 32]; }, part4);
+              float x0 = 1.f, x1 = 1.f;
+              if constexpr (SCALED) {
+                x0 = t * 8 + c0 < rows ? __ldg(a.x_scale + (size_t)source[t * 8 + c0] * S + s) : 0.f;
+                x1 = t * 8 + c0 + 1 < rows ? __ldg(a.x_scale + (size_t)source[t * 8 + c0 + 1] * S + s) : 0.f;
+              }
+              acc[m][t][0] = fmaf(part4[0], SCALED ? g0 * x0 : g0, acc[m][t][0]);
+              acc[m][t][1] = fmaf(part4[1], SCALED ? g0 * x1 : g0, acc[m][t][1]);
+              acc[m][t][2] = fmaf(part4[2], SCALED ? g1 * x0 : g1, acc[m][t][2]);
+              acc[m][t][3] = fmaf(part4[3], SCALED ? g1 * x1 : g1, acc[m][t][3]);
             }
-            acc[m][t][0] = fmaf(part[0], SCALED ? g0 * x0 : g0, acc[m][t][0]);
-            acc[m][t][1] = fmaf(part[1], SCALED ? g0 * x1 : g0, acc[m][t][1]);
-            acc[m][t][2] = fmaf(part[2], SCALED ? g1 * x0 : g1, acc[m][t][2]);
-            acc[m][t][3] = fmaf(part[3], SCALED ? g1 * x1 : g1, acc[m][t][3]);
           }
-        }
+      }
+      slot = slot + 1 == kStages ? 0 : slot + 1;
     }
-    // the halves' sums meet through shared memory: [warp of the first half][value][lane]
     ptx::cp_async_wait<0>();
-    __syncthreads();
-    float* sums = reinterpret_cast<float*>(stage) + (warp % kManyTiles) * MATS * kTilesN * 4 * 32 + lane;
-    if (half == 1) {
+    float* sums = reinterpret_cast<float*>(stage) + (warp % WIDE) * VALUES * 32 + lane;  // [warp][value][lane]
+    if constexpr (SPLIT == 2) {  // the halves' sums meet through shared memory
+      __syncthreads();
+      if (part == 1) {
 #pragma unroll
-      for (int v = 0; v < MATS * kTilesN * 4; ++v) sums[v * 32] = acc[v / (kTilesN * 4)][v / 4 % kTilesN][v % 4];
+        for (int v = 0; v < VALUES; ++v) sums[v * 32] = acc[v / (TILES * 4)][v / 4 % TILES][v % 4];
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (half == 0 && live) {
+    if (part == 0 && live) {
 #pragma unroll
-      for (int t = 0; t < kTilesN; ++t)
+      for (int t = 0; t < TILES; ++t)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int i = t * 8 + c0 + c % 2, o = out0 + lane / 4 + (c / 2) * 8;
-          if (i >= n) continue;
-          const float v = acc[0][t][c] + sums[(t * 4 + c) * 32];
+        for (int v = 0; v < 4; ++v) {
+          const int i = t * 8 + c0 + v % 2, o = out0 + lane / 4 + (v / 2) * 8;
+          if (i >= rows) continue;
+          float y = acc[0][t][v], z = acc[MATS - 1][t][v];
+          if constexpr (SPLIT == 2) {
+            y += sums[(t * 4 + v) * 32];
+            z += sums[((MATS - 1) * TILES * 4 + t * 4 + v) * 32];
+          }
           if constexpr (GATEUP) {
             __nv_bfloat16 plane[PA];
-            const float u = acc[MATS - 1][t][c] + sums[((MATS - 1) * kTilesN * 4 + t * 4 + c) * 32];
-            split_planes<PA>(v * sigmoidf_(v) * u, plane);
+            split_planes<PA>(y * sigmoidf_(y) * z, plane);
 #pragma unroll
             for (int p = 0; p < PA; ++p)
               static_cast<__nv_bfloat16*>(a.out)[((size_t)p * a.rows + list[i]) * a.N + paired(o)] = plane[p];
           } else {
-            static_cast<float*>(a.out)[(size_t)list[i] * a.N + o] = v;
+            static_cast<float*>(a.out)[(size_t)list[i] * a.N + o] = y;
           }
         }
     }
-    if (n < kPass) return;
-    __syncthreads();  // list and the stages are rewritten
   }
 }
 
@@ -925,29 +960,32 @@ void few(const W4Ffn& p, cudaStream_t st) {
 }
 
 template <int P, int PA, int G, bool GATEUP, bool SCALED>
-void many_product(const ManyArgs& a, int tokens, cudaStream_t st) {
-  const int bytes = kStages * 2 * kTilesN * 4 * 32 * P * 16;
+void many_product(const ManyArgs& a, cudaStream_t st) {
+  constexpr int WIDE = kWide<P, GATEUP>;
+  constexpr int bytes = kStages * (kWarps / WIDE) * (kPass<P> / 8) * 4 * 32 * P * 16;
   static bool ready[64] = {};
-  allow_shared(w4_many_kernel<P, PA, G, GATEUP, SCALED>, bytes, ready);
-  const dim3 grid((a.N + kManyTiles * kTile - 1) / (kManyTiles * kTile), a.rows < a.E ? a.rows : a.E,
-                  tokens < 256 ? (tokens + kPass - 1) / kPass : 8);
-  launch_early(w4_many_kernel<P, PA, G, GATEUP, SCALED>, grid, kWarps * 32, bytes, st, a);
+  allow_shared(w4_many_kernel<P, PA, G, GATEUP, SCALED, WIDE>, bytes, ready);
+  const long long items = (long long)most_units(a.rows, a.E, kPass<P>) * ((a.N + WIDE * kTile - 1) / (WIDE * kTile));
+  const long long blocks = 2ll * num_sms();
+  launch_early(w4_many_kernel<P, PA, G, GATEUP, SCALED, WIDE>, dim3((unsigned)(items < blocks ? items : blocks)), kWarps * 32, bytes, st, a);
 }
 
 template <typename X, typename T, int G>
 void many(const W4Ffn& p, cudaStream_t st) {
   constexpr int PX = Acts<X>::kPlanes, PA = kActPlanes<T>;
+  static_assert(kPass<PX> == kPass<PA>, "one plan for both products");
   const long long eights = (long long)p.T * p.h / 8;
-  w4_planes_kernel<X><<<(unsigned)((eights + 255) / 256), 256, 0, st>>>(static_cast<const X*>(p.x), eights,
-                                                                       static_cast<__nv_bfloat16*>(p.x_planes));
+  ManyPlan* plan = static_cast<ManyPlan*>(p.plan);
+  w4_prepare_kernel<X><<<(unsigned)((eights + 255) / 256 + 1), 256, 0, st>>>(
+      static_cast<const X*>(p.x), eights, static_cast<__nv_bfloat16*>(p.x_planes), p.topk_idx, p.T * p.k, p.E, kPass<PA>, plan);
   count_launch(st);
-  const ManyArgs up{static_cast<const __nv_bfloat16*>(p.x_planes), p.x_scale, p.topk_idx, p.T * p.k, p.k, p.T, p.E, p.h, p.f,
+  const ManyArgs up{static_cast<const __nv_bfloat16*>(p.x_planes), p.x_scale, plan, p.T * p.k, p.k, p.T, p.E, p.h, p.f,
                     {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
                      {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, p.a};
-  many_product<PX, PA, G, true, sizeof(X) == 1>(up, p.T, st);
-  const ManyArgs down{static_cast<const __nv_bfloat16*>(p.a), nullptr, p.topk_idx, p.T * p.k, 1, p.T * p.k, p.E, p.f, p.h,
+  many_product<PX, PA, G, true, sizeof(X) == 1>(up, st);
+  const ManyArgs down{static_cast<const __nv_bfloat16*>(p.a), nullptr, plan, p.T * p.k, 1, p.T * p.k, p.E, p.f, p.h,
                       {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.rows};
-  many_product<PA, PA, G, false, false>(down, p.T, st);
+  many_product<PA, PA, G, false, false>(down, st);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.T, (p.h / 4 + 255) / 256);
   cfg.blockDim = dim3(256);
@@ -979,14 +1017,15 @@ void run(const W4Ffn& p, cudaStream_t st) {
 
 }  // namespace
 
-size_t w4_scratch(int dtype, long long T, long long k, int h, int f, W4Scratch* at) {
+size_t w4_scratch(int dtype, long long T, long long k, int h, int E, int f, W4Scratch* at) {
   auto round = [](size_t b) { return (b + 255) & ~size_t(255); };
   W4Scratch s;
   s.a = 0;
   s.rows = s.a + round((size_t)T * k * f * 2 * (dtype == MOE_BF16 ? 2 : 3));
   s.x_planes = s.rows + round((size_t)T * k * h * sizeof(float));
+  s.plan = s.x_planes + round((size_t)T * h * 2 * (dtype == MOE_BF16 ? 1 : 3));
   if (at != nullptr) *at = s;
-  return s.x_planes + round((size_t)T * h * 2 * (dtype == MOE_BF16 ? 1 : 3));
+  return s.plan + round(16 + sizeof(int) * (3 * (size_t)most_units((int)(T * k), E, dtype == MOE_BF16 ? kPass<2> : kPass<3>) + T * k));
 }
 
 void launch_expert_ffn_w4(int dtype, const W4Ffn& p, cudaStream_t st) {
