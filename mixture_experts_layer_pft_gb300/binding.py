@@ -74,11 +74,12 @@ class MoEError(RuntimeError):
 
 
 _lib = None
+_marshal = None  # the module that checks tensors and takes their addresses (csrc/marshal.cpp)
 
 
 def lib() -> ctypes.CDLL:
     """Load libmoe_pft.so once; raise if it is not built."""
-    global _lib
+    global _lib, _marshal
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is not built: run __graft_entry__.build() first")
@@ -87,6 +88,9 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
+        from . import _marshal as M
+
+        _marshal = M
         _lib = L
     return _lib
 
@@ -322,20 +326,18 @@ def moe_gshard_combine(combine_w, ye, y, ws):
 
 
 def _check(t, name, dtype, shape):
-    """Refuse a tensor whose type or shape the call would misread (None passes); returns its pointer."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    return _p(t)
+    """Refuse a tensor whose type, shape or place the call would misread (None passes); returns its address."""
+    if _marshal is None:
+        lib()
+    return _marshal.pointer(t, name, dtype, shape)
 
 
 def moe_add_rmsnorm(x, residual, gamma, eps, s, y, q, q_scale, rstd, ws):
     """s = x + residual (both None: s is x) and its RMSNorm: y in x's dtype and/or q (float8_e4m3fn) with
     q_scale [T, ceil(h/128)] fp32; rstd [T] fp32 (or None) is what the backward needs."""
-    shape, dt = tuple(x.shape), x.dtype
+    shape, dt = x.shape, x.dtype
     T, h = shape
-    _call("moe_add_rmsnorm", _p(x), _check(residual, "residual", dt, shape), _check(gamma, "gamma", torch.float32, (h,)),
+    _call("moe_add_rmsnorm", _check(x, "x", dt, shape), _check(residual, "residual", dt, shape), _check(gamma, "gamma", torch.float32, (h,)),
           eps, T, h, _dtype_code(x), _check(s, "s", dt, shape), _check(y, "y", dt, shape),
           _check(q, "q", torch.float8_e4m3fn, shape), _check(q_scale, "q_scale", torch.float32, (T, (h + 127) // 128)),
           _check(rstd, "rstd", torch.float32, (T,)), _p(ws), ws.numel(), _stream())
@@ -343,26 +345,11 @@ def moe_add_rmsnorm(x, residual, gamma, eps, s, y, q, q_scale, rstd, ws):
 
 def moe_add_rmsnorm_bwd(dy, s, gamma, rstd, ds_add, ds, dgamma, ws):
     """ds = ds_add (or 0) + the norm's gradient for dy; dgamma [h] fp32."""
-    shape, dt = tuple(s.shape), s.dtype
+    shape, dt = s.shape, s.dtype
     T, h = shape
-    _call("moe_add_rmsnorm_bwd", _check(dy, "dy", dt, shape), _p(s), _check(gamma, "gamma", torch.float32, (h,)),
+    _call("moe_add_rmsnorm_bwd", _check(dy, "dy", dt, shape), _check(s, "s", dt, shape), _check(gamma, "gamma", torch.float32, (h,)),
           _check(rstd, "rstd", torch.float32, (T,)), _check(ds_add, "ds_add", dt, shape), T, h, _dtype_code(s),
           _check(ds, "ds", dt, shape), _check(dgamma, "dgamma", torch.float32, (h,)), _p(ws), ws.numel(), _stream())
-
-
-def _pointers(tensors, n, name, dtypes, sizes):
-    """A C array of the n tensors' device pointers; dtypes and sizes are what each must have."""
-    if len(tensors) != n:
-        raise ValueError(f"{name}: {len(tensors)} tensors for {n} parameters")
-    a = (ctypes.c_void_p * n)()
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        if t.dtype != dtypes[i] or t.numel() != sizes[i] or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {sizes[i]} {dtypes[i]}, got "
-                             f"{t.numel()} {t.dtype}")
-        a[i] = t.data_ptr()
-    return a
 
 
 def moe_adamw_step(params, grads, masters, m, v, m_scale, v_scale, weight_decay, lr, step, grad_scale, beta1, beta2,
@@ -372,24 +359,13 @@ def moe_adamw_step(params, grads, masters, m, v, m_scale, v_scale, weight_decay,
     value per 256 elements) float8_e4m3fn m and float8_e5m2 v.  ``weight_decay``: a number, or one per tensor.  ``lr``
     (fp32[1]), ``step`` (int32[1], this step's number) and ``grad_scale`` (fp32[1] or None) are on the device."""
     n = len(params)
-    dts = [t.dtype for t in params]
-    sizes = [t.numel() for t in params]
-    codes = (ctypes.c_int32 * n)(*[_dtype_code(t) for t in params])
-    f32 = [torch.float32] * n
-    q8 = m_scale is not None
-    blocks = [(s + 255) // 256 for s in sizes] if q8 else None
-    if (v_scale is not None) != q8:
-        raise ValueError("m_scale and v_scale go together")
+    if _marshal is None:
+        lib()
+    p, g, masters, m, v, m_scale, v_scale, sizes, codes = _marshal.optimizer(params, grads, masters, m, v, m_scale, v_scale)
     wd = (ctypes.c_float * n)(*(weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n))
-    _call("moe_adamw_step", n, _pointers(params, n, "params", dts, sizes), _pointers(grads, n, "grads", dts, sizes),
-          _pointers(masters, n, "masters", f32, sizes) if masters is not None else None,
-          _pointers(m, n, "m", [torch.float8_e4m3fn] * n if q8 else f32, sizes),
-          _pointers(v, n, "v", [torch.float8_e5m2] * n if q8 else f32, sizes),
-          _pointers(m_scale, n, "m_scale", f32, blocks) if q8 else None,
-          _pointers(v_scale, n, "v_scale", f32, blocks) if q8 else None,
-          (ctypes.c_int64 * n)(*sizes), wd, codes, 8 if q8 else 32, _check(lr, "lr", torch.float32, (1,)),
-          _check(step, "step", torch.int32, (1,)), _check(grad_scale, "grad_scale", torch.float32, (1,)), beta1, beta2, eps,
-          seed, _p(ws), ws.numel(), _stream())
+    _call("moe_adamw_step", n, p, g, masters, m, v, m_scale, v_scale, sizes, wd, codes, 32 if m_scale is None else 8,
+          _check(lr, "lr", torch.float32, (1,)), _check(step, "step", torch.int32, (1,)),
+          _check(grad_scale, "grad_scale", torch.float32, (1,)), beta1, beta2, eps, seed, _p(ws), ws.numel(), _stream())
 
 
 def moe_quantize_w4(W, group, q, scale, ws):

@@ -2,7 +2,8 @@
 
 Each translation unit compiles in parallel into ``_build/``; the objects are linked into one
 shared library next to this file.  Nothing is rebuilt when every object is newer than its
-source and the headers.
+source and the headers.  ``csrc/marshal.cpp``, the binding's argument checks, becomes the Python
+module ``_marshal.so`` beside it (host code; torch's headers).
 """
 
 from __future__ import annotations
@@ -18,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_pft.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 SOURCES = ["api.cu", "gather.cu", "route.cu", "pft.cu", "pft_noalloc.cu", "gemm_simt.cu", "gemm_tc.cu", "router_tc.cu", "gshard.cu", "gemm_f32tc.cu",
            "norm.cu", "adamw.cu", "w4.cu"]
@@ -44,6 +46,19 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _marshal_command(source: str) -> list:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            *[a for d in include for a in ("-isystem", d)], source, "-o", MARSHAL,
+            "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
     """Build (or reuse) libmoe_pft.so and return its path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -59,6 +74,10 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o])
 
+    source = os.path.join(CSRC, "marshal.cpp")
+    if force or _stale(MARSHAL, [source]):
+        jobs.insert(0, _marshal_command(source))
+
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -71,7 +90,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB, objs):
+    if force or _stale(LIB, objs):
         run([nvcc, *ARCH, "-shared", "-o", LIB, *objs])
     return LIB
 
