@@ -20,8 +20,8 @@ namespace {
 constexpr int kMaxVec = 4;       // 16-byte vectors of a row in one thread
 constexpr int kQGroup = 128;     // columns per scale of the 8-bit output
 
-constexpr int kRingElems = 16;     // elements of a row in one thread of the backward's ring kernel
 constexpr int kRingMaxStages = 8;
+constexpr int kRingThreads = 512;  // of a block, where several rows share one
 constexpr int kRingBytes = 200 * 1024;
 
 struct NormGeom {
@@ -186,27 +186,28 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_wide_kernel(const float*
 
 // The backward over a ring of row groups in shared memory.  One block an SM; its thread 0 keeps `stages` groups of
 // rows (dy, s, ds_add: each a contiguous piece of memory) under way as bulk copies, so that the reduction over a row
-// and the stores never leave HBM idle, and no register waits for a load.  16 elements of a row in a thread; gamma and
-// the thread's columns of dgamma stay in registers over all rows.
-template <typename T, int MAXT>
+// and the stores never leave HBM idle, and no register waits for a load.  16 elements of a row in a
+// thread; gamma and the thread's columns of dgamma stay in registers over all rows.
+template <typename T, int ELEMS, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* dy, const T* s, const float* __restrict__ gamma,
                                                                        const float* __restrict__ rstd, const T* ds_add, int T_,
                                                                        int h, int tpr, int rpb, int stages, T* ds,
                                                                        float* __restrict__ partial, int* status) {
-  constexpr int VN = Vec<T>::N, VPT = kRingElems / VN;
+  constexpr int VN = Vec<T>::N, VPT = ELEMS / VN;
   extern __shared__ uint4 ring[];
   __shared__ float red[2][32];
   __shared__ uint64_t full[kRingMaxStages];
   __shared__ int give_up;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lt = threadIdx.x % tpr, sub = threadIdx.x / tpr;
   const int nvec = h / VN, arrays = ds_add != nullptr ? 3 : 2, slot = rpb * nvec;
   const long long step = (long long)gridDim.x * rpb, first = (long long)blockIdx.x * rpb;
   const int turns = (int)((T_ - first + step - 1) / step);
-  auto issue = [&](int i) {
+  auto issue = [&](int i, int slot_i) {
     const long long t0 = first + i * step;
     const uint32_t bytes = (uint32_t)(t0 + rpb <= T_ ? rpb : (int)(T_ - t0)) * (uint32_t)nvec * 16u;
-    uint64_t* bar = &full[i % stages];
-    uint4* to = ring + (size_t)(i % stages) * 3 * slot;
+    uint64_t* bar = &full[slot_i];
+    uint4* to = ring + slot_i * 3 * slot;
     ptx::mbar_expect_tx(bar, bytes * arrays);
     ptx::bulk_load(ptx::smem_u32(to), reinterpret_cast<const uint4*>(dy) + t0 * nvec, bytes, bar);
     ptx::bulk_load(ptx::smem_u32(to + slot), reinterpret_cast<const uint4*>(s) + t0 * nvec, bytes, bar);
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* 
     give_up = 0;
     for (int i = 0; i < stages; ++i) ptx::mbar_init(&full[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    for (int i = 0; i < stages && i < turns; ++i) issue(i);
+    for (int i = 0; i < stages && i < turns; ++i) issue(i, i);
   }
   float w[VPT][VN], dg[VPT][VN];
 #pragma unroll
@@ -234,13 +235,17 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* 
   float rs_next = first + sub < T_ ? rstd[first + sub] : 0.f;
   __syncthreads();
   bool alive = true;
-  for (int i = 0; i < turns; ++i) {
-    const long long t = first + i * step + sub;
+  const int warp = threadIdx.x / kWarp, wpr = tpr / kWarp, w0 = warp / wpr * wpr;
+  long long t = first + sub;
+  uint4* out = reinterpret_cast<uint4*>(ds) + t * nvec;
+  int now = 0, before = stages - 1;  // the slots of this turn and the last
+  uint32_t parity = 0;
+  for (int i = 0; i < turns; ++i, t += step, out += step * nvec) {
     const bool on = t < T_;
     const float rs = rs_next;
-    rs_next = i + 1 < turns && t + step < T_ ? rstd[t + step] : 0.f;
-    const uint4* in = ring + (size_t)(i % stages) * 3 * slot + (size_t)sub * nvec;
-    const bool ok = ptx::mbar_wait(&full[i % stages], (i / stages) & 1, &give_up, status, 0);
+    rs_next = t + step < T_ ? rstd[t + step] : 0.f;
+    const uint4* in = ring + now * 3 * slot + sub * nvec;
+    const bool ok = ptx::mbar_try_wait(&full[now], parity) || ptx::mbar_wait(&full[now], parity, &give_up, status, 0);
     uint4 rd[VPT], rx[VPT];
     float dot = 0.f;
 #pragma unroll
@@ -262,18 +267,14 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* 
       }
     }
     dot = warp_sum(dot);
-    const int warp = threadIdx.x / kWarp, wpr = tpr / kWarp, w0 = warp / wpr * wpr;
     if (threadIdx.x % kWarp == 0) red[i & 1][warp] = dot;
     // every thread is past the stage of turn i - 1 here: it may be filled again
     if (!__syncthreads_and(ok)) {
       alive = false;
       break;
     }
-    if (threadIdx.x == 0 && i > 0 && i - 1 + stages < turns) issue(i - 1 + stages);
-    if (wpr > 1) {
-      dot = 0.f;
-      for (int k = 0; k < wpr; ++k) dot += red[i & 1][w0 + k];
-    }
+    if (threadIdx.x == 0 && i > 0 && i - 1 + stages < turns) issue(i - 1 + stages, before);
+    if (wpr > 1) dot = warp_sum(threadIdx.x % kWarp < wpr ? red[i & 1][w0 + threadIdx.x % kWarp] : 0.f);
     const float mean = dot * inv_h;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
@@ -290,7 +291,12 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* 
       }
 #pragma unroll
       for (int c = 0; c < VN; ++c) o[c] = fmaf(rs, fmaf(-(x[c] * rs), mean, d[c] * w[u][c]), o[c]);
-      reinterpret_cast<uint4*>(ds)[t * nvec + v] = pack(o, T());
+      out[v] = pack(o, T());
+    }
+    before = now;
+    if (++now == stages) {
+      now = 0;
+      parity ^= 1;
     }
   }
   if (!alive) {  // copies may still be on their way into this block's shared memory: let them land
@@ -321,9 +327,10 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* 
 }
 
 // dgamma[c] = sum over the `parts` partials, p ascending within each of 8 strips, strips ascending.
-__global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ partial, int parts, int h,
+__global__ void __launch_bounds__(256) dgamma_kernel(const float* partial, int parts, int h,
                                                      float* __restrict__ dgamma) {
   __shared__ float red[8][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials
   const int c = blockIdx.x * 32 + threadIdx.x % 32, strip = threadIdx.x / 32;
   float sum = 0.f;
   if (c < h)
@@ -349,9 +356,10 @@ void launch_fwd(const void* x, const void* residual, const float* gamma, float e
 
 // The ring needs two stages of a row group at least: rows up to 34,128 bytes (all of bf16's, fp32 up to 8,528 columns).
 // Wider rows go through the kernel that loads them into registers.
-template <typename T, int MAXT>
+template <typename T, int ELEMS, int MAXT>
 int launch_ring(const void* dy, const void* s, const float* gamma, const float* rstd, const void* ds_add, int T_, int h,
-                void* ds, float* partial, int tpr, int rpb, int* status, cudaStream_t st) {
+                void* ds, float* partial, int* status, cudaStream_t st) {
+  const int tpr = ((h + ELEMS - 1) / ELEMS + 31) / 32 * 32, rpb = tpr >= kRingThreads ? 1 : kRingThreads / tpr;
   const int stage = 3 * rpb * h * (int)sizeof(T);
   int stages = kRingBytes / stage;
   if (stages > kRingMaxStages) stages = kRingMaxStages;
@@ -361,10 +369,10 @@ int launch_ring(const void* dy, const void* s, const float* gamma, const float* 
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !ready[dev]) {
-    cudaFuncSetAttribute(add_rmsnorm_bwd_ring_kernel<T, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    cudaFuncSetAttribute(add_rmsnorm_bwd_ring_kernel<T, ELEMS, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
-  add_rmsnorm_bwd_ring_kernel<T, MAXT><<<blocks, tpr * rpb, (size_t)stages * stage, st>>>(
+  add_rmsnorm_bwd_ring_kernel<T, ELEMS, MAXT><<<blocks, tpr * rpb, (size_t)stages * stage, st>>>(
       static_cast<const T*>(dy), static_cast<const T*>(s), gamma, rstd, static_cast<const T*>(ds_add), T_, h, tpr, rpb, stages,
       static_cast<T*>(ds), partial, status);
   return blocks;
@@ -375,9 +383,8 @@ void launch_bwd(const void* dy, const void* s, const float* gamma, const float* 
                 void* ds, float* dgamma, float* partial, int* status, cudaStream_t st) {
   int parts = 0;
   if (2 * 3 * h * (int)sizeof(T) <= kRingBytes) {
-    const int tpr = ((h + kRingElems - 1) / kRingElems + 31) / 32 * 32, rpb = tpr >= 512 ? 1 : 512 / tpr;
-    parts = tpr <= 512 ? launch_ring<T, 512>(dy, s, gamma, rstd, ds_add, T_, h, ds, partial, tpr, rpb, status, st)
-                       : launch_ring<T, 1024>(dy, s, gamma, rstd, ds_add, T_, h, ds, partial, tpr, rpb, status, st);
+    parts = h <= 8192 ? launch_ring<T, 16, 512>(dy, s, gamma, rstd, ds_add, T_, h, ds, partial, status, st)
+                      : launch_ring<T, 16, 1024>(dy, s, gamma, rstd, ds_add, T_, h, ds, partial, status, st);
   } else if constexpr (sizeof(T) == 4) {
     const NormGeom g = norm_geom(h / Vec<T>::N);  // a row a block at these widths
     parts = T_ < kNormMaxParts ? T_ : kNormMaxParts;
@@ -386,7 +393,17 @@ void launch_bwd(const void* dy, const void* s, const float* gamma, const float* 
         static_cast<float*>(ds), partial);
   }
   count_launch(st);
-  dgamma_kernel<<<(h + 31) / 32, 256, 0, st>>>(partial, parts, h, dgamma);
+  // may begin while the rows are still at work (it waits for them by itself): its launch costs no time of its own
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((h + 31) / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, dgamma_kernel, (const float*)partial, parts, h, dgamma);
   count_launch(st);
 }
 
