@@ -40,7 +40,7 @@ template <int P, bool GATEUP> constexpr int kWide = GATEUP || P == 3 ? 4 : 8;
 constexpr int kStages = 3;      // turns of activations in shared memory, many form
 constexpr int kFewBytes = 100 * 1024;  // shared memory for the few form's activations
 constexpr int kFewSteps = 128;         // of a warp: kFewBytes / (128 inputs x 2.25 bytes) / 8, and one more an expert
-constexpr int kUpBlocks = 3, kUpAhead = 1, kDownBlocks = 3, kDownAhead = 2;  // one token: blocks an SM, steps under way
+constexpr int kUpBlocks = 4, kUpAhead = 1, kDownAhead = 4;  // one token: blocks an SM, steps of weights under way
 
 struct W4Mat {
   const unsigned char* q;
@@ -224,15 +224,20 @@ __device__ __forceinline__ float int_scale(uint32_t amax, float* inverse) {
   *inverse = m < 0x1p-100f || amax >= 0x7f800000u ? 0.f : kMostInt<P> / m;
   return amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : m < 0x1p-100f ? 0.f : m * (1.0f / (16.0f * kMostInt<P>));
 }
-// The bytes of an integer, the highest first.
+// Byte planes of four integers, the highest first: a lower plane's bytes are the integers' own (read as signed they are up
+// to 128 too small, which is added before the next shift).
 template <int P>
-__device__ __forceinline__ void int_bytes(int q, int* digit) {
+__device__ __forceinline__ void int_planes(int q0, int q1, int q2, int q3, uint32_t* plane) {
+  auto bytes = [](int x0, int x1, int x2, int x3, uint32_t from) {  // byte 0 or 1 of each
+    return __byte_perm(__byte_perm(x0, x1, from), __byte_perm(x2, x3, from), 0x5410);
+  };
 #pragma unroll
-  for (int p = P - 1; p > 0; --p) {
-    digit[p] = (int)(signed char)q;
-    q = (q - digit[p]) >> 8;
+  for (int p = P - 1; p > 1; --p) {
+    plane[p] = bytes(q0, q1, q2, q3, 0x0040);
+    q0 = (q0 + 128) >> 8; q1 = (q1 + 128) >> 8; q2 = (q2 + 128) >> 8; q3 = (q3 + 128) >> 8;
   }
-  digit[0] = q;
+  plane[1] = bytes(q0, q1, q2, q3, 0x0040);
+  plane[0] = bytes(q0 + 128, q1 + 128, q2 + 128, q3 + 128, 0x0051);
 }
 // Place of input i of 16 in its 16 bytes: per 8 inputs the even ones, then the odd ones, as a word's nibbles lie.
 __device__ __forceinline__ int byte_place(int i) { return (i & 8) | ((i & 1) << 2) | ((i >> 1) & 3); }
@@ -399,17 +404,15 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few
       float scale = int_scale<P>(amax, &inverse);
       if constexpr (sizeof(X) == 1) scale *= __ldg(a.x_scale + (size_t)token[r] * S + i / 8);
       scales[r * blocks + i] = scale;
-      uint32_t word[P][4] = {};
+      uint32_t word[4][P];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        int digit[P];
-        int_bytes<P>(__float2int_rn(f[c] * inverse), digit);
-        const int to = byte_place(c);
-#pragma unroll
-        for (int p = 0; p < P; ++p) word[p][to / 4] |= (uint32_t)(digit[p] & 0xff) << (8 * (to % 4));
+      for (int c = 0; c < 4; ++c) {  // of eight inputs the even ones, then the odd ones
+        const float* v = f + c / 2 * 8 + (c & 1);
+        int_planes<P>(__float2int_rn(v[0] * inverse), __float2int_rn(v[2] * inverse), __float2int_rn(v[4] * inverse),
+                      __float2int_rn(v[6] * inverse), word[c]);
       }
 #pragma unroll
-      for (int p = 0; p < P; ++p) acts[(r * blocks + i) * P + p] = make_uint4(word[p][0], word[p][1], word[p][2], word[p][3]);
+      for (int p = 0; p < P; ++p) acts[(r * blocks + i) * P + p] = make_uint4(word[0][p], word[1][p], word[2][p], word[3][p]);
     }
   }
   __syncthreads();
@@ -463,10 +466,10 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few
     const float sx = int_scale<P>(amax, &inverse);
     if (on) {
       const size_t row = (size_t)token[r] * a.k + __ffsll(bits_of(mask, token[r], a.k)) - 1, block = row * (a.N / 16) + blockIdx.x * 2 + t;
-      int digit[P];
-      int_bytes<P>(__float2int_rn(value * inverse), digit);
+      uint32_t plane[P];
+      int_planes<P>(__float2int_rn(value * inverse), 0, 0, 0, plane);
 #pragma unroll
-      for (int p = 0; p < P; ++p) a.bytes[(block * P + p) * 16 + byte_place(o)] = (unsigned char)digit[p];
+      for (int p = 0; p < P; ++p) a.bytes[(block * P + p) * 16 + byte_place(o)] = (unsigned char)plane[p];
       if (o == 0) a.scales[block] = sx;
     }
   }
@@ -474,8 +477,8 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few
 
 // y of 16 outputs for all tokens: the steps of all experts' products over the warps, each token's sum over its experts in
 // registers.
-template <typename T, int P, int G, int ROWS>
-__global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kDownBlocks : 2) w4_few_down_kernel(const __grid_constant__ FewArgs a) {
+template <typename T, int P, int G, int ROWS, int BLOCKS>
+__global__ void __launch_bounds__(kWarps * 32, BLOCKS) w4_few_down_kernel(const __grid_constant__ FewArgs a) {
   constexpr int AHEAD = kDownAhead;
   extern __shared__ uint4 acts[];  // `a`: bytes [row][8 S][P][16], then scales [row][8 S]
   __shared__ float red[kWarps][kTile][ROWS + (ROWS > 1)];
@@ -557,10 +560,12 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kDownBlocks : 2) w4_f
     }
   }
   wait_dependency();  // `a` is read from here on; the weights above are nobody's output
+  // copies alone, so that no thread waits for one before it starts the next
   for (int r = 0; r < rows; ++r) {
     const uint4* from = reinterpret_cast<const uint4*>(a.bytes) + (size_t)r * (a.K / 16) * P;
     for (int i = threadIdx.x; i < a.K / 16 * P; i += kWarps * 32) ptx::cp_async_16(ptx::smem_u32(acts + r * blocks * P + i), from + i, 16);
-    for (int i = threadIdx.x; i < a.K / 16; i += kWarps * 32) scales[r * blocks + i] = a.scales[(size_t)r * (a.K / 16) + i];
+    const float* from_scale = a.scales + (size_t)r * (a.K / 16);
+    for (int i = threadIdx.x; i < a.K / 16; i += kWarps * 32) ptx::cp_async_4(ptx::smem_u32(scales + r * blocks + i), from_scale + i);
   }
   ptx::cp_async_commit();
   ptx::cp_async_wait<0>();
@@ -949,14 +954,23 @@ void few(const W4Ffn& p, cudaStream_t st) {
   const FewArgs up{p.x, p.x_scale, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.h, p.f,
                    {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
                     {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, bytes, scales, nullptr, p.status};
-  static bool ready[2][64] = {};
+  static bool ready[3][64] = {};
   allow_shared(w4_few_up_kernel<X, P, G, ROWS>, kFewBytes, ready[0]);
   w4_few_up_kernel<X, P, G, ROWS><<<dim3(p.f / (2 * kTile), p.T * p.k), kWarps * 32, few_bytes<T>(p.T, p.h), st>>>(up);
   count_launch(st);
   const FewArgs down{nullptr, nullptr, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.f, p.h,
                      {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, bytes, scales, p.y, p.status};
-  allow_shared(w4_few_down_kernel<T, P, G, ROWS>, kFewBytes, ready[1]);
-  launch_early(w4_few_down_kernel<T, P, G, ROWS>, dim3(p.h / kTile), kWarps * 32, few_bytes<T>(p.T * p.k, p.f), st, down);
+  // One token's second kernel with three blocks an SM spills some of its registers, which a grid of more than two an SM is
+  // glad to pay (Large layer: 46 us for both kernels, 51 with two) and a smaller one is not (Small layer: 17 and 14 us).
+  const size_t shared = few_bytes<T>(p.T * p.k, p.f);
+  const int blocks = p.h / kTile;
+  if (ROWS == 1 && blocks > 2 * num_sms()) {
+    allow_shared(w4_few_down_kernel<T, P, G, ROWS, ROWS == 1 ? 3 : 2>, kFewBytes, ready[2]);
+    launch_early(w4_few_down_kernel<T, P, G, ROWS, ROWS == 1 ? 3 : 2>, dim3(blocks), kWarps * 32, shared, st, down);
+  } else {
+    allow_shared(w4_few_down_kernel<T, P, G, ROWS, 2>, kFewBytes, ready[1]);
+    launch_early(w4_few_down_kernel<T, P, G, ROWS, 2>, dim3(blocks), kWarps * 32, shared, st, down);
+  }
 }
 
 template <int P, int PA, int G, bool GATEUP, bool SCALED>
