@@ -362,7 +362,11 @@ def moe_adamw_step(params, grads, masters, m, v, m_scale, v_scale, weight_decay,
     if _marshal is None:
         lib()
     p, g, masters, m, v, m_scale, v_scale, sizes, codes = _marshal.optimizer(params, grads, masters, m, v, m_scale, v_scale)
-    wd = (ctypes.c_float * n)(*(weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n))
+    if not isinstance(weight_decay, (list, tuple)):
+        weight_decay = [weight_decay] * n
+    elif len(weight_decay) != n:
+        raise ValueError(f"weight_decay: {len(weight_decay)} numbers for {n} parameters")
+    wd = (ctypes.c_float * n)(*weight_decay)
     _call("moe_adamw_step", n, p, g, masters, m, v, m_scale, v_scale, sizes, wd, codes, 32 if m_scale is None else 8,
           _check(lr, "lr", torch.float32, (1,)), _check(step, "step", torch.int32, (1,)),
           _check(grad_scale, "grad_scale", torch.float32, (1,)), beta1, beta2, eps, seed, _p(ws), ws.numel(), _stream())

@@ -31,6 +31,7 @@ const at::Tensor* tensor_of(PyObject* o, const char* name) {
 }
 
 bool on_device(const at::Tensor& t, const char* name) {
+  if (t.layout() != at::kStrided) return refuse(PyExc_ValueError, std::string(name) + ": tensor must be strided");
   if (!t.is_cuda()) return refuse(PyExc_ValueError, std::string(name) + ": tensor must be on a CUDA device");
   if (!t.is_contiguous()) return refuse(PyExc_ValueError, std::string(name) + ": tensor must be contiguous");
   return true;
@@ -158,9 +159,23 @@ PyObject* optimizer(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return out;
 }
 
+// torch reports by exception what a tensor cannot answer (a nested one its sizes, one without memory its address): none may
+// pass through the interpreter.
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  try {
+    return F(self, args, n);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+  }
+  return nullptr;
+}
+
 PyMethodDef methods[] = {
-    {"pointer", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(pointer)), METH_FASTCALL, "address of a checked tensor"},
-    {"optimizer", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(optimizer)), METH_FASTCALL, "arrays of an optimizer step"},
+    {"pointer", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<pointer>)), METH_FASTCALL, "address of a checked tensor"},
+    {"optimizer", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<optimizer>)), METH_FASTCALL, "arrays of an optimizer step"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "argument marshalling of the binding", -1, methods, nullptr, nullptr, nullptr, nullptr};
 

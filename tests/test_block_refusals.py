@@ -107,6 +107,25 @@ def test_binding_refuses_other_types_and_shapes(B):
         B._check(meta(4, 2, dtype=f8), "y", bf, (4, 2))
 
 
+def test_tensors_without_an_address_raise_and_do_not_end_the_process(B):
+    sparse = torch.zeros(4, 4).to_sparse()
+    nested = torch.nested.nested_tensor([torch.zeros(2), torch.zeros(3)])
+    for t in (sparse, nested, torch.empty(4, 4, device="meta"), torch.zeros(4, 4).t()):
+        with pytest.raises(ValueError):
+            B._check(t, "x", torch.float32, (4, 4))
+    with pytest.raises((TypeError, ValueError)):
+        B._check("no tensor", "x", torch.float32, (4, 4))
+    one = torch.zeros(8)
+    for wd in ([0.1, 0.2], []):
+        with pytest.raises(ValueError):
+            B.moe_adamw_step([one], [one], None, [one], [one], None, None, wd, one[:1], torch.ones(1, dtype=torch.int32), None, 0.9,
+                             0.99, 1e-8, 0, torch.zeros(256, dtype=torch.uint8))
+    for bad in ([sparse], [nested], ["x"], 3):
+        with pytest.raises((TypeError, ValueError)):
+            B.moe_adamw_step(bad, bad, None, bad, bad, None, None, 0.1, one[:1], torch.ones(1, dtype=torch.int32), None, 0.9, 0.99,
+                             1e-8, 0, torch.zeros(256, dtype=torch.uint8))
+
+
 def test_workspace_sizes(B):
     bf = torch.bfloat16
     for op in (B.MOE_OP_ADD_RMSNORM, B.MOE_OP_ADAMW):
