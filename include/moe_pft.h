@@ -443,8 +443,8 @@ int moe_quantize_w4(const void* W, int E, int K, int N, int dtype, int group, vo
  * [E,h,ceil(f/group)].  y: [T,h] dtype.  Sums are fp32 over the exact 4-bit values (a group's sum is
  * scaled once); a is kept to 16 (MOE_BF16) or 24 significant bits.  For few tokens (up to 8 and 64 rows) y sums
  * the experts in ascending order instead of j's.  An id outside [0,E) sets MOE_STATUS_BAD_INDEX and adds nothing.
- * An expert's weights are read once for every 32 of its rows
- * (MOE_F32: 16).  Requires h % 32 == 0, f % 32 == 0, h*f < 2^32,
+ * With more tokens an expert's weights are
+ * unpacked once for every 16 of its rows.  Requires h % 32 == 0, f % 32 == 0, h*f < 2^32,
  * 1 <= k <= E <= 1024 and T*k <= 65536.
  */
 int moe_expert_ffn_w4(const void* x, const float* x_scale, const int32_t* topk_idx, const float* topk_w,

@@ -358,13 +358,15 @@ void launch_fwd(const void* x, const void* residual, const float* gamma, float e
 // Wider rows go through the kernel that loads them into registers.
 template <typename T, int ELEMS, int MAXT>
 int launch_ring(const void* dy, const void* s, const float* gamma, const float* rstd, const void* ds_add, int T_, int h,
-                void* ds, float* partial, int* status, cudaStream_t st) {
+                void* ds, float* dgamma, float* partial, int* status, cudaStream_t st) {
   const int tpr = ((h + ELEMS - 1) / ELEMS + 31) / 32 * 32, rpb = tpr >= kRingThreads ? 1 : kRingThreads / tpr;
   const int stage = 3 * rpb * h * (int)sizeof(T);
   int stages = kRingBytes / stage;
   if (stages > kRingMaxStages) stages = kRingMaxStages;
   const int need = (T_ + rpb - 1) / rpb, most = num_sms() < kNormMaxParts ? num_sms() : kNormMaxParts;
-  const int blocks = need < most ? need : most;
+  // two turns of one block, whose sum is dgamma itself, are quicker than two blocks and a second kernel
+  const int blocks = need <= 2 ? 1 : need < most ? need : most;
+  if (blocks == 1) partial = dgamma;
   static bool ready[64] = {};  // per device: the attribute is set once
   int dev = 0;
   cudaGetDevice(&dev);
@@ -383,8 +385,8 @@ void launch_bwd(const void* dy, const void* s, const float* gamma, const float* 
                 void* ds, float* dgamma, float* partial, int* status, cudaStream_t st) {
   int parts = 0;
   if (2 * 3 * h * (int)sizeof(T) <= kRingBytes) {
-    parts = h <= 8192 ? launch_ring<T, 16, 512>(dy, s, gamma, rstd, ds_add, T_, h, ds, partial, status, st)
-                      : launch_ring<T, 16, 1024>(dy, s, gamma, rstd, ds_add, T_, h, ds, partial, status, st);
+    parts = h <= 8192 ? launch_ring<T, 16, 512>(dy, s, gamma, rstd, ds_add, T_, h, ds, dgamma, partial, status, st)
+                      : launch_ring<T, 16, 1024>(dy, s, gamma, rstd, ds_add, T_, h, ds, dgamma, partial, status, st);
   } else if constexpr (sizeof(T) == 4) {
     const NormGeom g = norm_geom(h / Vec<T>::N);  // a row a block at these widths
     parts = T_ < kNormMaxParts ? T_ : kNormMaxParts;
@@ -393,6 +395,7 @@ void launch_bwd(const void* dy, const void* s, const float* gamma, const float* 
         static_cast<float*>(ds), partial);
   }
   count_launch(st);
+  if (parts == 1 && 2 * 3 * h * (int)sizeof(T) <= kRingBytes) return;  // the ring's one block wrote dgamma
   // may begin while the rows are still at work (it waits for them by itself): its launch costs no time of its own
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((h + 31) / 32);

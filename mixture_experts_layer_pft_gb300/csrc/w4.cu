@@ -17,8 +17,7 @@
 //
 // Two forms.  Up to 8 tokens and 64 rows, as far as their activations fit in shared memory ("few"): two launches; token t is column t of every product, warps split the
 // inputs, and the second kernel adds its outputs over all experts in registers, so no row is written but `a`.  Above
-// ("many"): an expert's rows in units of 32 (fp32: 16) through shared memory, warps side by side over 64 outputs and two
-// halves of the inputs, experts' output rows to scratch, and a combine.
+// ("many"): an expert's rows in units of 16 through shared memory, experts' output rows to scratch, and a combine.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -33,11 +32,9 @@ constexpr int kWarps = 8;
 constexpr int kTile = 16;       // outputs of a warp
 constexpr int kStep = 128;      // inputs of a warp's step
 constexpr int kFewTokens = 8, kFewRows = 64;
-template <int P> constexpr int kPass = P == 3 ? 16 : 32;  // rows of a unit of the many form, activations in P planes
-// Warps side by side over the outputs, many form (64 tokens of the Medium layer, up / down: 4 / 8 236 us, 4 / 4 273, 8 / 8
-// 229; 13 fp32 ones of the long-sequence layer, whose items are few: 84, 68 and 89).
-template <int P, bool GATEUP> constexpr int kWide = GATEUP || P == 3 ? 4 : 8;
-constexpr int kStages = 3;      // turns of activations in shared memory, many form
+constexpr int kTurn = 2;         // steps between barriers of the many form
+constexpr int kStages = 4;       // turns of activations in shared memory
+constexpr int kPass = 16;        // rows of a unit of the many form
 constexpr int kFewBytes = 100 * 1024;  // shared memory for the few form's activations
 constexpr int kFewSteps = 128;         // of a warp: kFewBytes / (128 inputs x 2.25 bytes) / 8, and one more an expert
 constexpr int kUpBlocks = 4, kUpAhead = 1, kDownAhead = 4;  // one token: blocks an SM, steps of weights under way
@@ -150,25 +147,33 @@ struct LanePlace {
   }
 };
 
-// A group's words (their A operands f) with one column tile of activations, all planes.  One or two planes: one chain of
-// sums a group.  Three (fp32): the small planes in a chain of their own, as the tensor core's sums round towards zero.
+// A group's words (their A operands f) with two column tiles of activations, all planes.  One or two planes: one chain of
+// sums a tile.  Three (fp32): the small planes in a chain of their own, as the tensor core's sums round towards zero.
 template <int P, int G, typename LOAD>
-__device__ __forceinline__ void group_product(const uint32_t (*f)[2][4], LOAD load, float part[4]) {
-  float low[4];
+__device__ __forceinline__ void group_pair(const uint32_t (*f)[2][4], LOAD load, float part[2][4]) {
+  float low[2][4];
 #pragma unroll
   for (int j = 0; j < G / 32; ++j)
 #pragma unroll
     for (int p = P - 1; p >= 0; --p) {
-      const uint4 u = load(j, p);
-      const bool apart = P == 3 && p > 0;
-      float* to = apart ? low : part;
-      if (j == 0 && (apart ? p == P - 1 : P == 3 || p == P - 1)) mma_bf16_first(to, f[j][0], u.x, u.y);
-      else mma_bf16(to, f[j][0], u.x, u.y);
-      mma_bf16(to, f[j][1], u.z, u.w);
+      const bool apart = P == 3 && p > 0, first = j == 0 && (apart ? p == P - 1 : P == 3 || p == P - 1);
+      uint4 u[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) u[t] = load(t, j, p);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float* to = apart ? low[t] : part[t];
+        if (first) mma_bf16_first(to, f[j][0], u[t].x, u[t].y);
+        else mma_bf16(to, f[j][0], u[t].x, u[t].y);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) mma_bf16(apart ? low[t] : part[t], f[j][1], u[t].z, u[t].w);
     }
   if constexpr (P == 3) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) part[c] += low[c];
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) part[t][c] += low[t][c];
   }
 }
 
@@ -611,20 +616,20 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS) w4_few_down_kernel(const 
 
 // ------------------------------------------------------------------------------------ many rows
 
-// What the products work through: units of an expert and up to `pass` of its rows, and the rows by expert.
+// What the products work through: units of an expert and up to kPass of its rows, and the rows by expert.
 struct ManyPlan {
   int units, pad[3];
   int unit[1];  // units x (expert, first place in the rows' list, rows), then the list
 };
-__host__ __device__ __forceinline__ int most_units(int rows, int E, int pass) {  // an expert's last unit may be short
-  return (rows < E ? rows : E) + rows / pass;
+__host__ __device__ __forceinline__ int most_units(int rows, int E) {  // an expert's last unit may be short
+  return (rows < E ? rows : E) + rows / kPass;
 }
 
 // x [T, K] to paired bf16 planes [P][T][K]; block 0 makes the plan.  The place of a row in its expert's part of the list
 // is whichever its atomic gives it: a row is a column of its own in every product, and no result depends on which.
 template <typename X>
 __global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x, long long eights, __nv_bfloat16* __restrict__ out,
-                                                         const int* __restrict__ topk_idx, int rows, int E, int pass, ManyPlan* plan) {
+                                                         const int* __restrict__ topk_idx, int rows, int E, ManyPlan* plan) {
   constexpr int P = Acts<X>::kPlanes;
   launch_dependents();
   if (blockIdx.x > 0) {
@@ -648,7 +653,7 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x
   if (warp == 0) {  // rows and units before each expert
     int before = 0, units = 0;
     for (int e0 = 0; e0 < E; e0 += kWarp) {
-      const int e = e0 + lane, c = e < E ? count[e] : 0, u = (c + pass - 1) / pass;
+      const int e = e0 + lane, c = e < E ? count[e] : 0, u = (c + kPass - 1) / kPass;
       int cs = c, us = u;
 #pragma unroll
       for (int o = 1; o < kWarp; o <<= 1) {
@@ -660,8 +665,8 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x
         for (int i = 0; i < u; ++i) {
           int* to = plan->unit + 3 * (units + us - u + i);
           to[0] = e;
-          to[1] = before + cs - c + i * pass;
-          to[2] = min(c - i * pass, pass);
+          to[1] = before + cs - c + i * kPass;
+          to[2] = min(c - i * kPass, kPass);
         }
       }
       before += __shfl_sync(0xffffffffu, cs, kWarp - 1);
@@ -670,7 +675,7 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x
     if (lane == 0) plan->units = units;
   }
   __syncthreads();
-  int* list = plan->unit + 3 * most_units(rows, E, pass);
+  int* list = plan->unit + 3 * most_units(rows, E);
   for (int r = threadIdx.x; r < rows; r += 256) {
     const int e = __ldg(topk_idx + r);
     if ((unsigned)e < (unsigned)E) list[atomicAdd(&start[e], 1)] = r;
@@ -686,20 +691,22 @@ struct ManyArgs {
   void* out;               // gate/up: a's planes [PA][rows][N]; down: [rows, N] fp32
 };
 
-// Blocks take turns at the items, each WIDE tiles of outputs (one a warp) of a unit; with 4 tiles, warps 0-3 take the even
-// steps and 4-7 the odd ones.  A turn of the loop is a step of each.
-template <int P, int PA, int G, bool GATEUP, bool SCALED, int WIDE>
-__global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_constant__ ManyArgs a) {
-  constexpr int MATS = GATEUP ? 2 : 1, TILES = kPass<P> / 8, VALUES = MATS * TILES * 4, SPLIT = kWarps / WIDE;
-  constexpr int STEP = TILES * 4 * 32 * P;  // 16-byte pieces of a step: [row tile][word][plane][lane]
-  extern __shared__ uint4 stage[];          // [stage][step of the turn][STEP]
-  __shared__ int list[kPass<P>], source[kPass<P>];
-  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, part = warp / WIDE;
-  launch_dependents();
-  wait_dependency();
+// Blocks take turns at the items of a unit.  A warp has one tile of 16 outputs of one matrix (gate/up: half of the warps W1,
+// the other half W3), and every split-th step of it; a turn of the loop is kTurn steps.  With many items the tiles lie side
+// by side over the warps (split 1: 64 outputs of both matrices, or 128); with few, two warps share a tile's steps, so
+// that there are more and shorter items.  Which one follows from the number of units, known here alone: split 1
+// from one and a half items a block on (64 tokens of the Medium layer: 200 us, and 243 with 2; 13 fp32 ones of the
+// long-sequence layer: 87 and 71).
+template <int P, int PA, int G, bool GATEUP, bool SCALED, int SPLIT>
+__device__ __forceinline__ void many_items(const ManyArgs& a, uint4* stage, int* list, int* source) {
+  constexpr int MOST = GATEUP ? kWarps / 2 : kWarps, TILES = kPass / 8, VALUES = TILES * 4;
+  constexpr int STEP = TILES * 4 * 32 * P;  // 16-byte pieces of a step's activations: [row tile][word][plane][lane]
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, mat = warp / MOST;
+  const int S = (a.K + kStep - 1) / kStep, turns = (S + kTurn - 1) / kTurn;
+  constexpr int WIDE = MOST / SPLIT;
   const int across = (a.N + WIDE * kTile - 1) / (WIDE * kTile), items = a.plan->units * across;
-  const int S = (a.K + kStep - 1) / kStep, turns = (S + SPLIT - 1) / SPLIT;
-  const int* rows_by_expert = a.plan->unit + 3 * most_units(a.rows, a.E, kPass<P>);
+  const int tile = warp % MOST % WIDE, part = warp % MOST / WIDE;
+  const int* rows_by_expert = a.plan->unit + 3 * most_units(a.rows, a.E);
   // an item's expert, number of rows and, in thread i, its i-th row: read an item ahead
   int e = 0, n = 0, r = 0;
   auto look = [&](int item) {
@@ -711,8 +718,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_co
   };
   look(blockIdx.x);
   const LanePlace<G> lanes(0, a.K, lane);  // strides, and this lane's place in the first tile
-  const int c = threadIdx.x % (16 * SPLIT), r0 = threadIdx.x / (16 * SPLIT);  // this thread's piece of a turn's activations
-  constexpr int ROWS_FILL = kWarps * 32 / (16 * SPLIT), FILLS = kPass<P> / ROWS_FILL;
+  // this thread's pieces of a turn's activations: the same eight inputs of rows APART apart
+  const int c = threadIdx.x % (16 * kTurn), r0 = threadIdx.x / (16 * kTurn);
+  constexpr int APART = kWarps * 32 / (16 * kTurn), FILLS = kPass / APART;
   int word, quarter;
   place_of<G>(c % 16, &word, &quarter);
   const int c0 = (lane % 4) * 2;
@@ -722,41 +730,34 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_co
       list[threadIdx.x] = r;
       source[threadIdx.x] = r / a.k;
     }
-    const int out0 = (item % across * WIDE + warp % WIDE) * kTile, rows = n, tiles = (n + 7) / 8;
+    const int out0 = (item % across * WIDE + tile) * kTile, rows = n;
     const bool live = out0 < a.N;
-    const unsigned char* q[MATS];
-    const __nv_bfloat16* sc[MATS];
-#pragma unroll
-    for (int m = 0; m < MATS; ++m) {
-      q[m] = a.mat[m].q + ((size_t)e * a.N + (live ? out0 : 0)) * (a.K / 2) + lanes.q + part * (kStep / 2);
-      sc[m] = a.mat[m].s + ((size_t)e * a.N + (live ? out0 : 0)) * ((a.K + G - 1) / G) + lanes.s + part * (kStep / G);
-    }
-    IntWeights<G, MATS> next;
+    const size_t row0 = (size_t)e * a.N + (live ? out0 : 0);
+    const unsigned char* q = a.mat[mat].q + row0 * (a.K / 2) + lanes.q + part * (kStep / 2);
+    const __nv_bfloat16* sc = a.mat[mat].s + row0 * ((a.K + G - 1) / G) + lanes.s + part * (kStep / G);
+    IntWeights<G, 1> w[2];
     int k0 = part * kStep;  // of the weights to load next
-    auto load = [&] {
-      if (k0 < a.K) next.load(q, sc, lanes.q8, lanes.s8, k0 + lanes.k, k0, a.K);
+    auto load = [&](IntWeights<G, 1>& to) {
+      if (k0 < a.K) to.load(&q, &sc, lanes.q8, lanes.s8, k0 + lanes.k, k0, a.K);
       k0 += SPLIT * kStep;
-#pragma unroll
-      for (int m = 0; m < MATS; ++m) {
-        q[m] += SPLIT * (kStep / 2);
-        sc[m] += SPLIT * (kStep / G);
-      }
+      q += SPLIT * (kStep / 2);
+      sc += SPLIT * (kStep / G);
     };
-    load();
+    load(w[0]);
+    load(w[1]);
     __syncthreads();
     look(item + gridDim.x);
     // a turn's activations: piece (row, eight) of plane p goes where lane (row % 8, quarter) reads it
     const __nv_bfloat16* from[FILLS];
 #pragma unroll
     for (int i = 0; i < FILLS; ++i)
-      from[i] = r0 + i * ROWS_FILL < rows ? a.x + (size_t)source[r0 + i * ROWS_FILL] * a.K + c * 8 : nullptr;
-    auto fill = [&](int turn, int slot) {
-      const uint32_t to = ptx::smem_u32(stage + (slot * SPLIT + c / 16) * STEP);
-      const int k = turn * SPLIT * kStep;
+      from[i] = r0 + i * APART < rows ? a.x + (size_t)source[r0 + i * APART] * a.K + c * 8 : nullptr;
+    auto fill = [&](int turn) {
+      const uint32_t to = ptx::smem_u32(stage + (turn % kStages * kTurn + c / 16) * STEP);
+      const int k = turn * kTurn * kStep;
 #pragma unroll
       for (int i = 0; i < FILLS; ++i) {
-        const int row = r0 + i * ROWS_FILL;
-        if (row >= tiles * 8) break;
+        const int row = r0 + i * APART;
         const bool in = from[i] != nullptr && k + c * 8 < a.K;
         const __nv_bfloat16* x = in ? from[i] + k : a.x;
 #pragma unroll
@@ -767,110 +768,131 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_co
     };
 #pragma unroll
     for (int t = 0; t < kStages - 1; ++t) {
-      if (t < turns) fill(t, t);
+      if (t < turns) fill(t);
       ptx::cp_async_commit();
     }
-    float acc[MATS][TILES][4];
+    float acc[TILES][4];
 #pragma unroll
-    for (int m = 0; m < MATS; ++m)
+    for (int t = 0; t < TILES; ++t)
 #pragma unroll
-      for (int t = 0; t < TILES; ++t)
+      for (int v = 0; v < 4; ++v) acc[t][v] = 0.f;
+    const int own = turns * kTurn / SPLIT;  // of a warp's steps, those beyond the inputs included
+    int turn = 0;
+    for (int o0 = 0; o0 < own; o0 += 2) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[m][t][v] = 0.f;
-    int slot = 0;
-    for (int turn = 0; turn < turns; ++turn) {
-      ptx::cp_async_wait<kStages - 2>();
-      __syncthreads();  // the turn's activations are there, and the stage before it has been read by all
-      if (turn + kStages - 1 < turns) fill(turn + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
-      ptx::cp_async_commit();
-      const IntWeights<G, MATS> w = next;
-      load();
-      const int s = turn * SPLIT + part;
-      if (s < S) {
-        const uint4* b = stage + (slot * SPLIT + part) * STEP + lane;
+      for (int d = 0; d < 2; ++d) {
+        if (o0 + d >= own) break;
+        if (d * SPLIT % kTurn == 0) {
+          ptx::cp_async_wait<kStages - 2>();
+          __syncthreads();  // the turn's activations are there, and the stage before it has been read by all
+          if (turn + kStages - 1 < turns) fill(turn + kStages - 1);
+          ptx::cp_async_commit();
+          ++turn;
+        }
+        const int s = (o0 + d) * SPLIT + part;
+        if (s >= S) continue;
+        const uint4* b = stage + s % (kStages * kTurn) * STEP + lane;
 #pragma unroll
-        for (int m = 0; m < MATS; ++m)
+        for (int i = 0; i < kStep / G; ++i) {
+          uint32_t f[G / 32][2][4];
 #pragma unroll
-          for (int i = 0; i < kStep / G; ++i) {
-            uint32_t f[G / 32][2][4];
+          for (int j = 0; j < G / 32; ++j) unpack_word(w[d].w[0][0][i * (G / 32) + j], w[d].w[0][1][i * (G / 32) + j], f[j]);
+          const float g0 = __bfloat162float(w[d].s[0][0][i]), g1 = __bfloat162float(w[d].s[0][1][i]);
+          if (i == kStep / G - 1) load(w[d]);
+          static_assert(TILES == 2, "a pair of row tiles");
+          float sum[2][4];  // two chains of dependent products at once; the second may be of no rows
+          group_pair<P, G>(f, [&](int u, int j, int p) { return b[((u * 4 + i * (G / 32) + j) * P + p) * 32]; }, sum);
 #pragma unroll
-            for (int j = 0; j < G / 32; ++j) unpack_word(w.w[m][0][i * (G / 32) + j], w.w[m][1][i * (G / 32) + j], f[j]);
-            const float g0 = __bfloat162float(w.s[m][0][i]), g1 = __bfloat162float(w.s[m][1][i]);
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-              if (t >= tiles) break;
-              float part4[4];
-              group_product<P, G>(f, [&](int j, int p) { return b[((t * 4 + i * (G / 32) + j) * P + p) * 32]; }, part4);
-              float x0 = 1.f, x1 = 1.f;
-              if constexpr (SCALED) {
-                x0 = t * 8 + c0 < rows ? __ldg(a.x_scale + (size_t)source[t * 8 + c0] * S + s) : 0.f;
-                x1 = t * 8 + c0 + 1 < rows ? __ldg(a.x_scale + (size_t)source[t * 8 + c0 + 1] * S + s) : 0.f;
-              }
-              acc[m][t][0] = fmaf(part4[0], SCALED ? g0 * x0 : g0, acc[m][t][0]);
-              acc[m][t][1] = fmaf(part4[1], SCALED ? g0 * x1 : g0, acc[m][t][1]);
-              acc[m][t][2] = fmaf(part4[2], SCALED ? g1 * x0 : g1, acc[m][t][2]);
-              acc[m][t][3] = fmaf(part4[3], SCALED ? g1 * x1 : g1, acc[m][t][3]);
+          for (int u = 0; u < 2; ++u) {
+            float x0 = 1.f, x1 = 1.f;
+            if constexpr (SCALED) {
+              const int row = u * 8 + c0;
+              x0 = row < rows ? __ldg(a.x_scale + (size_t)source[row] * S + s) : 0.f;
+              x1 = row + 1 < rows ? __ldg(a.x_scale + (size_t)source[row + 1] * S + s) : 0.f;
             }
-          }
-      }
-      slot = slot + 1 == kStages ? 0 : slot + 1;
-    }
-    ptx::cp_async_wait<0>();
-    float* sums = reinterpret_cast<float*>(stage) + (warp % WIDE) * VALUES * 32 + lane;  // [warp][value][lane]
-    if constexpr (SPLIT == 2) {  // the halves' sums meet through shared memory
-      __syncthreads();
-      if (part == 1) {
-#pragma unroll
-        for (int v = 0; v < VALUES; ++v) sums[v * 32] = acc[v / (TILES * 4)][v / 4 % TILES][v % 4];
-      }
-      __syncthreads();
-    }
-    if (part == 0 && live) {
-#pragma unroll
-      for (int t = 0; t < TILES; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int i = t * 8 + c0 + v % 2, o = out0 + lane / 4 + (v / 2) * 8;
-          if (i >= rows) continue;
-          float y = acc[0][t][v], z = acc[MATS - 1][t][v];
-          if constexpr (SPLIT == 2) {
-            y += sums[(t * 4 + v) * 32];
-            z += sums[((MATS - 1) * TILES * 4 + t * 4 + v) * 32];
-          }
-          if constexpr (GATEUP) {
-            __nv_bfloat16 plane[PA];
-            split_planes<PA>(y * sigmoidf_(y) * z, plane);
-#pragma unroll
-            for (int p = 0; p < PA; ++p)
-              static_cast<__nv_bfloat16*>(a.out)[((size_t)p * a.rows + list[i]) * a.N + paired(o)] = plane[p];
-          } else {
-            static_cast<float*>(a.out)[(size_t)list[i] * a.N + o] = y;
+            acc[u][0] = fmaf(sum[u][0], SCALED ? g0 * x0 : g0, acc[u][0]);
+            acc[u][1] = fmaf(sum[u][1], SCALED ? g0 * x1 : g0, acc[u][1]);
+            acc[u][2] = fmaf(sum[u][2], SCALED ? g1 * x0 : g1, acc[u][2]);
+            acc[u][3] = fmaf(sum[u][3], SCALED ? g1 * x1 : g1, acc[u][3]);
           }
         }
+      }
+    }
+    ptx::cp_async_wait<0>();
+    __syncthreads();
+    // the parts' and the matrices' sums meet through shared memory: [warp][value][lane]
+    float* sums = reinterpret_cast<float*>(stage) + lane;
+#pragma unroll
+    for (int v = 0; v < VALUES; ++v) sums[(warp * VALUES + v) * 32] = acc[v / 4][v % 4];
+    __syncthreads();
+    if (mat == 0 && part == 0 && live) {
+#pragma unroll
+      for (int v = 0; v < VALUES; ++v) {
+        float y = acc[v / 4][v % 4], z = GATEUP ? sums[((MOST + tile) * VALUES + v) * 32] : 0.f;
+#pragma unroll
+        for (int i = 1; i < SPLIT; ++i) {
+          y += sums[((i * WIDE + tile) * VALUES + v) * 32];
+          if constexpr (GATEUP) z += sums[((MOST + i * WIDE + tile) * VALUES + v) * 32];
+        }
+        const int i = v / 4 * 8 + c0 + v % 2, o = out0 + lane / 4 + (v % 4 / 2) * 8;
+        if (i >= rows) continue;
+        if constexpr (GATEUP) {
+          __nv_bfloat16 plane[PA];
+          split_planes<PA>(y * sigmoidf_(y) * z, plane);
+#pragma unroll
+          for (int p = 0; p < PA; ++p)
+            static_cast<__nv_bfloat16*>(a.out)[((size_t)p * a.rows + list[i]) * a.N + paired(o)] = plane[p];
+        } else {
+          static_cast<float*>(a.out)[(size_t)list[i] * a.N + o] = y;
+        }
+      }
     }
   }
 }
 
-// y[t] = sum_j topk_w[t,j] * rows[t*k+j], j ascending; a row of no expert counts as zeros.
+template <int P, int PA, int G, bool GATEUP, bool SCALED>
+__global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_constant__ ManyArgs a) {
+  extern __shared__ uint4 stage[];  // [stage][step of the turn][STEP]
+  __shared__ int list[kPass], source[kPass];
+  launch_dependents();
+  wait_dependency();
+  constexpr int OUTS = (GATEUP ? kWarps / 2 : kWarps) * kTile;
+  if (2 * a.plan->units * ((a.N + OUTS - 1) / OUTS) >= 3 * (int)gridDim.x) many_items<P, PA, G, GATEUP, SCALED, 1>(a, stage, list, source);
+  else many_items<P, PA, G, GATEUP, SCALED, 2>(a, stage, list, source);
+}
+
+// y[t] = sum_j topk_w[t,j] * rows[t*k+j], j ascending; a row of no expert counts as zeros.  The choices do not wait for the
+// products, and eight rows are under way at once (one after another they took 8 us for 64 tokens of the Medium layer).
 template <typename T>
 __global__ void __launch_bounds__(256) w4_combine_kernel(const float* rows, const int* __restrict__ topk_idx,
                                                          const float* __restrict__ topk_w, int k, int E, int h,
                                                          T* __restrict__ y, int* status) {
+  constexpr int ONCE = 8;
   const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 4;
-  wait_dependency();
-  if (c >= h) return;
+  const size_t r0 = (size_t)t * k;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < k; ++j) {
-    const size_t r = (size_t)t * k + j;
-    if ((unsigned)__ldg(topk_idx + r) >= (unsigned)E) {
-      if (c == 0) flag_status(status, MOE_STATUS_BAD_INDEX);
-      continue;
+  for (int j0 = 0; j0 < k; j0 += ONCE) {
+    bool in[ONCE];
+    float w[ONCE];
+#pragma unroll
+    for (int j = 0; j < ONCE; ++j) {
+      in[j] = j0 + j < k && (unsigned)__ldg(topk_idx + r0 + j0 + j) < (unsigned)E;
+      w[j] = j0 + j < k ? __ldg(topk_w + r0 + j0 + j) : 0.f;
+      if (j0 + j < k && !in[j] && c == 0) flag_status(status, MOE_STATUS_BAD_INDEX);
     }
-    const float w = __ldg(topk_w + r);
-    const float4 v = *reinterpret_cast<const float4*>(rows + r * h + c);
-    s.x = fmaf(w, v.x, s.x); s.y = fmaf(w, v.y, s.y); s.z = fmaf(w, v.z, s.z); s.w = fmaf(w, v.w, s.w);
+    if (j0 == 0) wait_dependency();
+    if (c >= h) continue;
+    float4 v[ONCE];
+#pragma unroll
+    for (int j = 0; j < ONCE; ++j)
+      v[j] = in[j] ? *reinterpret_cast<const float4*>(rows + (r0 + j0 + j) * h + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < ONCE; ++j) {
+      if (!in[j]) continue;
+      s.x = fmaf(w[j], v[j].x, s.x); s.y = fmaf(w[j], v[j].y, s.y); s.z = fmaf(w[j], v[j].z, s.z); s.w = fmaf(w[j], v[j].w, s.w);
+    }
   }
-  store4(y + (size_t)t * h + c, s);
+  if (c < h) store4(y + (size_t)t * h + c, s);
 }
 
 // W [E, K, N] -> q [E, N, K/2], scale [E, N, ceil(K/G)]: scale = bf16(amax / 7), nibble =
@@ -975,23 +997,21 @@ void few(const W4Ffn& p, cudaStream_t st) {
 
 template <int P, int PA, int G, bool GATEUP, bool SCALED>
 void many_product(const ManyArgs& a, cudaStream_t st) {
-  constexpr int WIDE = kWide<P, GATEUP>;
-  constexpr int bytes = kStages * (kWarps / WIDE) * (kPass<P> / 8) * 4 * 32 * P * 16;
+  constexpr int bytes = kStages * kTurn * (kPass / 8) * 4 * 32 * P * 16;
+  static_assert(bytes >= kWarps * kPass / 2 * 32 * 4, "the stages hold all warps' sums");
   static bool ready[64] = {};
-  allow_shared(w4_many_kernel<P, PA, G, GATEUP, SCALED, WIDE>, bytes, ready);
-  const long long items = (long long)most_units(a.rows, a.E, kPass<P>) * ((a.N + WIDE * kTile - 1) / (WIDE * kTile));
-  const long long blocks = 2ll * num_sms();
-  launch_early(w4_many_kernel<P, PA, G, GATEUP, SCALED, WIDE>, dim3((unsigned)(items < blocks ? items : blocks)), kWarps * 32, bytes, st, a);
+  allow_shared(w4_many_kernel<P, PA, G, GATEUP, SCALED>, bytes, ready);
+  const long long items = (long long)most_units(a.rows, a.E) * (a.N / kTile), blocks = 2ll * num_sms();
+  launch_early(w4_many_kernel<P, PA, G, GATEUP, SCALED>, dim3((unsigned)(items < blocks ? items : blocks)), kWarps * 32, bytes, st, a);
 }
 
 template <typename X, typename T, int G>
 void many(const W4Ffn& p, cudaStream_t st) {
   constexpr int PX = Acts<X>::kPlanes, PA = kActPlanes<T>;
-  static_assert(kPass<PX> == kPass<PA>, "one plan for both products");
   const long long eights = (long long)p.T * p.h / 8;
   ManyPlan* plan = static_cast<ManyPlan*>(p.plan);
   w4_prepare_kernel<X><<<(unsigned)((eights + 255) / 256 + 1), 256, 0, st>>>(
-      static_cast<const X*>(p.x), eights, static_cast<__nv_bfloat16*>(p.x_planes), p.topk_idx, p.T * p.k, p.E, kPass<PA>, plan);
+      static_cast<const X*>(p.x), eights, static_cast<__nv_bfloat16*>(p.x_planes), p.topk_idx, p.T * p.k, p.E, plan);
   count_launch(st);
   const ManyArgs up{static_cast<const __nv_bfloat16*>(p.x_planes), p.x_scale, plan, p.T * p.k, p.k, p.T, p.E, p.h, p.f,
                     {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
@@ -1039,7 +1059,7 @@ size_t w4_scratch(int dtype, long long T, long long k, int h, int E, int f, W4Sc
   s.x_planes = s.rows + round((size_t)T * k * h * sizeof(float));
   s.plan = s.x_planes + round((size_t)T * h * 2 * (dtype == MOE_BF16 ? 1 : 3));
   if (at != nullptr) *at = s;
-  return s.plan + round(16 + sizeof(int) * (3 * (size_t)most_units((int)(T * k), E, dtype == MOE_BF16 ? kPass<2> : kPass<3>) + T * k));
+  return s.plan + round(16 + sizeof(int) * (3 * (size_t)most_units((int)(T * k), E) + T * k));
 }
 
 void launch_expert_ffn_w4(int dtype, const W4Ffn& p, cudaStream_t st) {
