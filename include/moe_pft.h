@@ -439,13 +439,15 @@ int moe_quantize_w4(const void* W, int E, int K, int N, int dtype, int group, vo
  *   a = silu(W1_e x[t]) * (W3_e x[t]);  y[t] = sum_j topk_w[t,j] * W2_e a, e = topk_idx[t,j], j ascending.
  * x: [T,h] in x_dtype: the call's dtype, or MOE_E4M3 (dtype MOE_BF16 then) with x_scale [T,ceil(h/128)]
  * fp32, as moe_add_rmsnorm writes them; x_scale is NULL otherwise.  topk_idx: [T,k] int32, topk_w:
- * [T,k] fp32 (these three at any address of their type: rows of a larger batch may be passed as they are).  W1q, W3q: [E,f,h/2], W1s, W3s: [E,f,ceil(h/group)]; W2q: [E,h,f/2], W2s:
- * [E,h,ceil(f/group)].  y: [T,h] dtype.  Sums are fp32 over the exact 4-bit values (a group's sum is
- * scaled once); a is kept to 16 (MOE_BF16) or 24 significant bits.  For few tokens (up to 8 and 64 rows) y sums
- * the experts in ascending order instead of j's.  An id outside [0,E) sets MOE_STATUS_BAD_INDEX and adds nothing.
- * With more tokens an expert's weights are
- * unpacked once for every 16 of its rows.  Requires h % 32 == 0, f % 32 == 0, h*f < 2^32,
- * 1 <= k <= E <= 1024 and T*k <= 65536.
+ * [T,k] fp32 (these three at any address of their type: rows of a larger batch may be passed as they are).
+ * W1q, W3q: [E,f,h/2], W1s, W3s: [E,f,ceil(h/group)]; W2q: [E,h,f/2], W2s: [E,h,ceil(f/group)].  y: [T,h] dtype.
+ * Sums are fp32 over the exact 4-bit values, a group's sum is scaled once.  With up to 8 tokens and 64 rows that fit
+ * in shared memory, x and a are rounded to 16 (MOE_BF16) or 24 bits of the largest of 16 neighbours, and y sums the
+ * experts in ascending order instead of j's, whatever else is in the batch; otherwise x is read as it is and a keeps
+ * 16 or 24 significant bits, and the order of the fp32 sums may go by the batch's routing (deterministically).  An id
+ * outside [0,E) sets MOE_STATUS_BAD_INDEX and adds nothing.  A token with a value that is not a finite number gets NaN
+ * or infinities, and no other token does.
+ * Requires h % 32 == 0, f % 32 == 0, h*f < 2^32, 1 <= k <= E <= 1024 and T*k <= 65536.
  */
 int moe_expert_ffn_w4(const void* x, const float* x_scale, const int32_t* topk_idx, const float* topk_w,
                       const void* W1q, const void* W1s, const void* W3q, const void* W3s, const void* W2q,

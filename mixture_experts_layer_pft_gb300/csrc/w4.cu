@@ -2,22 +2,30 @@
 //
 //   W[n, i] = (nibble - 8) * scale[n, i / G];  a = silu(W1_e x) * (W3_e x);  y[t] = sum_j w_j W2_e a.
 //
-// With few rows an expert's product is bound by its weights' bytes, so each weight goes straight from HBM into the
-// registers of the warp that uses it, once for all rows of a pass.  The product runs on the tensor cores with the outputs
-// as M = 16 and the token rows as N = 8: the nibbles become bf16 (128 + nibble by an OR into the mantissa, minus 136:
-// exact), a group's sum is kept apart in fp32 and scaled once, so no weight is rounded.  Activations go in as exact bf16
-// values or planes of them: x in bf16 or e4m3 as it is, x in fp32 as its three planes, `a` as three (fp32) or two (bf16
-// layers: 16 significant bits) of its fp32 value.  tcgen05 would want the weights unpacked into shared memory, and a
-// group's scale inside them, which rounds; at these row counts the tensor pipe is not what bounds either path.
+// The floor is the active experts' bytes: 182 MB, 27 us, for one token of the Large layer (h 7168, f 2048, k 8 of 256).  What
+// bounds the kernels instead is instructions: a byte of weights is two products, and turning nibbles into operands costs
+// more than multiplying them.  Measured on this GPU, instructions a clock and SM: dp4a, LOP3, IMAD, I2F and bf16x2 FMA 1.9
+// each, mma.sync bf16 16x8x16 0.50, mma.sync s8 16x8x32 0.06.  Two forms follow from that.
+//
+// "Few" (up to 8 tokens and 64 rows whose activations fit in shared memory): integers through dp4a, see below.  Two launches:
+// the first writes `a`, the second adds each token's outputs over its experts in registers; it starts early and has its
+// first weights under way while the first still runs.  Large layer, one token in 8 bits: 46 us (58% of the floor's rate;
+// tensor cores in this place 86 us).  Small layer (h 2048, f 1408, 6 of 64): 14 us, of which the launches, the chain from
+// topk_idx to y and the host are most.
+//
+// "Many": tensor cores with 16 outputs as M and token rows as N.  The nibbles become bf16 (128 + nibble by an OR into the
+// mantissa, minus 136: exact), a group's sum is kept apart in fp32 and scaled once, so no weight is rounded.  Activations go
+// in as exact bf16 values or planes of them: x in bf16 or e4m3 as it is, x in fp32 as its three planes, `a` as three (fp32)
+// or two (bf16 layers: 16 significant bits) of its fp32 value.  An expert's rows come in units of 16; experts' output rows
+// go to scratch, and a combine adds them.  64 tokens of the Medium layer (h 5120, f 1536, 6 of 128, skewed): 212 us against
+// a floor of 36: unpacking once for 16 rows, the latency of the products and uneven experts.  (tcgen05 would want the
+// unpacked weights in shared memory and its sums read back after each group, as a scale inside the operands would round
+// them; it would pay from some 32 rows an expert on, and is not built.)
 //
 // A warp's step is 16 outputs x 128 inputs.  The sum over inputs may run in any order, so lane (g, q) = (lane / 4, lane % 4)
 // takes for outputs g and g + 8 the G/4 consecutive inputs of each group that are contiguous in its 4-bit row: the weights
-// need no other layout than [output][input / 2].  Two nibbles of a word sit 16 bits apart as inputs i and i + 4, so eight
-// activations go in as (0,4) (1,5) (2,6) (3,7); activation planes are stored in that order ("paired" below).
-//
-// Two forms.  Up to 8 tokens and 64 rows, as far as their activations fit in shared memory ("few"): two launches; token t is column t of every product, warps split the
-// inputs, and the second kernel adds its outputs over all experts in registers, so no row is written but `a`.  Above
-// ("many"): an expert's rows in units of 16 through shared memory, experts' output rows to scratch, and a combine.
+// need no other layout than [output][input / 2].  Two nibbles of a word sit 16 bits apart as inputs i and i + 4, so for the
+// tensor cores eight activations go in as (0,4) (1,5) (2,6) (3,7); planes are stored in that order ("paired" below).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -37,7 +45,9 @@ constexpr int kStages = 4;       // turns of activations in shared memory
 constexpr int kPass = 16;        // rows of a unit of the many form
 constexpr int kFewBytes = 100 * 1024;  // shared memory for the few form's activations
 constexpr int kFewSteps = 128;         // of a warp: kFewBytes / (128 inputs x 2.25 bytes) / 8, and one more an expert
-constexpr int kUpBlocks = 4, kUpAhead = 1, kDownAhead = 4;  // one token: blocks an SM, steps of weights under way
+// One token: blocks an SM, and steps of weights under way in a warp.  Large / Small layer, both kernels: 4, 1 and 4 46 / 14 us;
+// 3, 1 and 2 57 / 18; 2, 2 and 4 59 / 14.
+constexpr int kUpBlocks = 4, kUpAhead = 1, kDownAhead = 4;
 
 struct W4Mat {
   const unsigned char* q;
@@ -192,6 +202,9 @@ __device__ __forceinline__ void place_of(int c, int* word, int* quarter) {
 // too, of 16 bits (bf16 and e4m3 activations) or 24 (fp32), as P signed bytes, with one fp32 scale per 16 inputs: an
 // activation is off by at most 2^-16 (2^-24) of the largest of its 16, far below what the output's type can show.
 // Sums of 16 products are exact in 32 bits.
+//
+// Also measured for a token of the Large layer: bulk copies of the rows into shared memory (pieces of 512 bytes: 76 us, of
+// 1024: 70, the copies are too small), and a warp along 1024 inputs of one output instead of 16 outputs x 128 (57 to 75).
 
 struct FewArgs {
   const void* x;          // gate/up: [T, K] of X; down: nothing
@@ -222,12 +235,12 @@ __device__ __forceinline__ unsigned long long bits_of(unsigned long long mask, i
 template <int P> constexpr float kMostInt = P == 2 ? 32630.f : 8355000.f;
 
 // Scale of 16 values whose largest magnitude has the pattern `amax`, and its inverse.  Values that are no finite numbers
-// make it NaN; below 2^-100 all count as zeros.  The scale carries the 1/16 of the weights' bytes.
+// make it NaN; below 2^-90 all count as zeros.  The scale carries the 1/16 of the weights' bytes.
 template <int P>
 __device__ __forceinline__ float int_scale(uint32_t amax, float* inverse) {
   const float m = __uint_as_float(amax);
-  *inverse = m < 0x1p-100f || amax >= 0x7f800000u ? 0.f : kMostInt<P> / m;
-  return amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : m < 0x1p-100f ? 0.f : m * (1.0f / (16.0f * kMostInt<P>));
+  *inverse = m < 0x1p-90f || amax >= 0x7f800000u ? 0.f : kMostInt<P> / m;
+  return amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : m < 0x1p-90f ? 0.f : m * (1.0f / (16.0f * kMostInt<P>));
 }
 // Byte planes of four integers, the highest first: a lower plane's bytes are the integers' own (read as signed they are up
 // to 128 too small, which is added before the next shift).
@@ -641,7 +654,7 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x
     for (int p = 0; p < P; ++p) reinterpret_cast<uint4*>(out)[p * eights + i] = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
     return;
   }
-  __shared__ int count[1024], start[1024], total[2];
+  __shared__ int count[1024], start[1024];
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   for (int e = threadIdx.x; e < E; e += 256) count[e] = 0;
   __syncthreads();
