@@ -8,7 +8,7 @@
 // Both are bound by HBM: every array moves once.  Forward: a row stays in the registers of its `tpr` threads (16-byte
 // vectors, at most kMaxVec a thread).  4096 x 7168 bf16 with residual, y and q: 265 MB in 46 us, 85% of the measured copy
 // rate (57 us where the loads of a row were mixed with its stores); one row: 4 us, all latency.  Backward: a ring of bulk
-// copies, see there; the same rows with ds_add: 235 MB in 44 us (79%), dgamma's second kernel included.  Sums run in fp32
+// copies, see there; the same rows with ds_add: 235 MB in 42 us (82%), dgamma's second kernel included.  Sums run in fp32
 // in a fixed order: no atomics, bitwise reproducible.
 #include <cuda_fp8.h>
 
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_wide_kernel(const float*
 // The backward over a ring of row groups in shared memory.  One block an SM; its thread 0 keeps `stages` groups of
 // rows (dy, s, ds_add: each a contiguous piece of memory) under way as bulk copies, so that the reduction over a row
 // and the stores never leave HBM idle, and no register waits for a load (a kernel that loads
-// rows into registers took 147 us where this one takes 40).  16 elements of a row in a
+// rows into registers took 147 us where this one takes 35).  16 elements of a row in a
 // thread; gamma and the thread's columns of dgamma stay in registers over all rows.
 template <typename T, int ELEMS, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* dy, const T* s, const float* __restrict__ gamma,
@@ -330,22 +330,25 @@ __global__ void __launch_bounds__(MAXT, 1) add_rmsnorm_bwd_ring_kernel(const T* 
   }
 }
 
-// dgamma[c] = sum over the `parts` partials, p ascending within each of 8 strips, strips ascending.
-__global__ void __launch_bounds__(256) dgamma_kernel(const float* partial, int parts, int h,
-                                                     float* __restrict__ dgamma) {
-  __shared__ float red[8][32];
+// dgamma[c] = sum over the `parts` partials: p ascending by 32 within each of 32 strips (at most ten loads of a thread, under
+// way together), then the strips by halves.  8 strips took 5.3 us beside the Large layer's 35 us of rows.
+__global__ void __launch_bounds__(1024) dgamma_kernel(const float* partial, int parts, int h, float* __restrict__ dgamma) {
+  __shared__ float red[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, strip = threadIdx.x / 32;
-  float sum = 0.f;
-  if (c < h)
-    for (int p = strip; p < parts; p += 8) sum += partial[(size_t)p * h + c];
-  red[strip][threadIdx.x % 32] = sum;
-  __syncthreads();
-  if (strip == 0 && c < h) {
+  const int lane = threadIdx.x % 32, strip = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+  constexpr int MOST = (kNormMaxParts + 31) / 32;
+  float v[MOST], sum = 0.f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) sum += red[i][threadIdx.x];
-    dgamma[c] = sum;
+  for (int i = 0; i < MOST; ++i) {
+    const int p = strip + 32 * i;
+    v[i] = c < h && p < parts ? partial[(size_t)p * h + c] : 0.f;
   }
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) sum += v[i];
+  red[strip][lane] = sum;
+  __syncthreads();
+  sum = warp_sum(red[lane][strip]);  // of column `strip`
+  if (lane == 0 && blockIdx.x * 32 + strip < h) dgamma[blockIdx.x * 32 + strip] = sum;
 }
 
 template <typename T>
@@ -403,7 +406,7 @@ void launch_bwd(const void* dy, const void* s, const float* gamma, const float* 
   // may begin while the rows are still at work (it waits for them by itself): its launch costs no time of its own
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((h + 31) / 32);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(1024);
   cfg.stream = st;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
