@@ -15,8 +15,8 @@
 // instructions an element and the conversions are the rest).  adamw_kernel's tensors come by launch
 // argument: 57 small ones in one launch, 24 us with the host's part.
 //
-// Every operation that decides a code is one
-// correctly rounded fp32 operation (no contraction), so the codes follow from the formulas.
+// Every operation that decides a code is one correctly rounded fp32 operation (no contraction), so the codes
+// follow from the formulas.
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kOptBlock = 256;     // elements of one scale, handled by one warp
 constexpr int kWarps = 8;
+constexpr int kBlocks8 = 5, kBlocks32 = 2;  // thread blocks an SM, 8- and 32-bit states
 
 template <int N>
 struct AdamwArgs {
@@ -357,7 +358,7 @@ __device__ __forceinline__ void run_warp(const AdamwArgs<N>& a, const AdamwTenso
 }
 
 template <int N, bool Q8>
-__global__ void __launch_bounds__(kWarps * 32, Q8 ? 5 : 2) adamw_kernel(const __grid_constant__ AdamwArgs<N> a) {
+__global__ void __launch_bounds__(kWarps * 32, Q8 ? kBlocks8 : kBlocks32) adamw_kernel(const __grid_constant__ AdamwArgs<N> a) {
   int lo = 0, hi = a.n - 1;  // the tensor of this thread block
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -384,11 +385,18 @@ void launch_some(const AdamwTensor* t, int n, int first_tensor, const AdamwScala
   // A warp's setup (its tensor, the bias corrections) costs about a block's work.  With 8-bit states, bound by the
   // instructions, 16 blocks share it (the Small layer: 4 blocks 1721 us, 8 1626, 16 1585, 32 1568); with 32-bit states,
   // bound by HBM, shorter runs keep its many streams closer together (4: 2244, 8: 2277, 16: 2286, 32: 2372).  Where
-  // that leaves too few warps for the SMs, a warp takes fewer.
+  // that leaves too few warps for the SMs, a warp takes fewer.  Long runs are then evened out to whole rounds of the
+  // warps that the SMs hold, for a last round of a few warps takes as long as a full one (16.5 M parameters with 8-bit
+  // states: 1.3 rounds of 8 blocks 63.5 us, one of 11 blocks 57.9).  Short ones are not: there more warps than one round
+  // cover each other's setup (4.5 M parameters: 2 blocks 24.0 us, an even 3 25.0).
   long long all = 0, chunks = 0;
   for (int i = 0; i < n; ++i) all += (t[i].numel + kOptBlock - 1) / kOptBlock;
   a.blocks_per_warp = c.q8 ? 16 : 4;
   while (a.blocks_per_warp > 1 && all < (long long)num_sms() * 32 * a.blocks_per_warp) a.blocks_per_warp /= 2;
+  if (a.blocks_per_warp >= 8) {
+    const long long round = (long long)num_sms() * kWarps * kBlocks8, rounds = (all + 16 * round - 1) / (16 * round);
+    a.blocks_per_warp = (int)((all + round * rounds - 1) / (round * rounds));
+  }
   const long long chunk = (long long)kOptBlock * kWarps * a.blocks_per_warp;
   for (int i = 0; i < n; ++i) {
     a.t[i] = t[i];
