@@ -441,12 +441,12 @@ int moe_quantize_w4(const void* W, int E, int K, int N, int dtype, int group, vo
  * fp32, as moe_add_rmsnorm writes them; x_scale is NULL otherwise.  topk_idx: [T,k] int32, topk_w:
  * [T,k] fp32 (these three at any address of their type: rows of a larger batch may be passed as they are).
  * W1q, W3q: [E,f,h/2], W1s, W3s: [E,f,ceil(h/group)]; W2q: [E,h,f/2], W2s: [E,h,ceil(f/group)].  y: [T,h] dtype.
- * Sums are fp32 over the exact 4-bit values, a group's sum is scaled once.  With up to 8 tokens and 64 rows that fit
- * in shared memory, x and a are rounded to 16 (MOE_BF16) or 24 bits of the largest of 16 neighbours, and y sums the
- * experts in ascending order instead of j's, whatever else is in the batch; otherwise x is read as it is and a keeps
- * 16 or 24 significant bits, and the order of the fp32 sums may go by the batch's routing (deterministically).  An id
- * outside [0,E) sets MOE_STATUS_BAD_INDEX and adds nothing.  A token with a value that is not a finite number gets NaN
- * or infinities, and no other token does.
+ * Sums are fp32 over the exact 4-bit values, a group's sum is scaled once.  One token (k <= 64), and up to 8 tokens with
+ * T*k <= 12, that fit in shared memory: x and a are rounded to 16 (MOE_BF16) or 24 bits of the largest of 16 neighbours, and y sums the experts in ascending order instead of j's, whatever else is in the batch.
+ * Otherwise x is read as it is (its values below 2^-34 of the largest of 128 neighbours apart), a keeps 11 or 23
+ * significant bits, and the order of the fp32 sums may go by the batch's routing (deterministically).  An id outside
+ * [0,E) sets MOE_STATUS_BAD_INDEX and adds nothing.  A token with a value that is not a finite number gets NaN or
+ * infinities, and no other token does.
  * Requires h % 32 == 0, f % 32 == 0, h*f < 2^32, 1 <= k <= E <= 1024 and T*k <= 65536.
  */
 int moe_expert_ffn_w4(const void* x, const float* x_scale, const int32_t* topk_idx, const float* topk_w,

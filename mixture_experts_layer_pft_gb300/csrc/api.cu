@@ -686,7 +686,7 @@ int moe_expert_ffn_w4(const void* x, const float* x_scale, const int32_t* topk_i
   W4Scratch at;
   w4_scratch(dtype, T, k, h, E, f, &at);
   const W4Ffn p{x, x_scale, topk_idx, topk_w, W1q, W1s, W3q, W3s, W2q, W2s, T, k, E, h, f, group, y, base + at.a,
-                reinterpret_cast<float*>(base + at.rows), base + at.x_planes, base + at.plan, status_of(ws)};
+                reinterpret_cast<float*>(base + at.rows), base + at.x_planes, base + at.a_planes, base + at.plan, status_of(ws)};
   launch_expert_ffn_w4(dtype, p, (cudaStream_t)stream);
   return check_launch("moe_expert_ffn_w4");
 }

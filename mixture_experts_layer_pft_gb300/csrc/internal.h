@@ -131,7 +131,7 @@ void launch_adamw(const AdamwTensor* t, int n, int first_tensor, const AdamwScal
 // w4.cu -- routed experts over 4-bit weights.  Scratch: a's bf16 planes ([2 or 3][T*k, f]), the experts' output rows
 // ([T*k, h] fp32), x's planes ([1 or 3][T, h]) and the rows by expert; w4_scratch: its bytes, and the parts' offsets.
 struct W4Scratch {
-  size_t a, rows, x_planes, plan;
+  size_t a, rows, x_planes, a_planes, plan;
 };
 size_t w4_scratch(int dtype, long long T, long long k, int h, int E, int f, W4Scratch* at);
 struct W4Ffn {
@@ -145,6 +145,7 @@ struct W4Ffn {
   void* a;
   float* rows;
   void* x_planes;
+  void* a_planes;
   void* plan;
   int* status;
 };

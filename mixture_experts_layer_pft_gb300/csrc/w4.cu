@@ -7,25 +7,29 @@
 // more than multiplying them.  Measured on this GPU, instructions a clock and SM: dp4a, LOP3, IMAD, I2F and bf16x2 FMA 1.9
 // each, mma.sync bf16 16x8x16 0.50, mma.sync s8 16x8x32 0.06.  Two forms follow from that.
 //
-// "Few" (up to 8 tokens and 64 rows whose activations fit in shared memory): integers through dp4a, see below.  Two launches:
+// "Few" (one token, or up to 8 and 12 rows, whose activations fit in shared memory): integers through dp4a, see below.  Two launches:
 // the first writes `a`, the second adds each token's outputs over its experts in registers; it starts early and has its
 // first weights under way while the first still runs.  Large layer, one token in 8 bits: 46 us (58% of the floor's rate;
 // tensor cores in this place 86 us).  Small layer (h 2048, f 1408, 6 of 64): 14 us, of which the launches, the chain from
 // topk_idx to y and the host are most.
 //
-// "Many": tensor cores with 16 outputs as M and token rows as N.  The nibbles become bf16 (128 + nibble by an OR into the
-// mantissa, minus 136: exact), a group's sum is kept apart in fp32 and scaled once, so no weight is rounded.  Activations go
-// in as exact bf16 values or planes of them: x in bf16 or e4m3 as it is, x in fp32 as its three planes, `a` as three (fp32)
-// or two (bf16 layers: 16 significant bits) of its fp32 value.  An expert's rows come in units of 16; experts' output rows
-// go to scratch, and a combine adds them.  64 tokens of the Medium layer (h 5120, f 1536, 6 of 128, skewed): 212 us against
-// a floor of 36: unpacking once for 16 rows, the latency of the products and uneven experts.  (tcgen05 would want the
-// unpacked weights in shared memory and its sums read back after each group, as a scale inside the operands would round
-// them; it would pay from some 32 rows an expert on, and is not built.)
+// "Many": tensor cores with 16 outputs as M and token rows as N.  A nibble n masked out of its word and read as f16 is the
+// subnormal n 2^-24, exactly: eight nibbles are operands after five instructions (bf16 operands would take eleven; e4m3
+// ones, which n 2^-9 would be as easily, three, but mma.sync does 0.28 of those a clock and SM once they change).
+// Activations go in as planes of f16 over one scale per row and step, which is a power of two: x in e4m3 and bf16 as one,
+// exactly; x in fp32 as two, of 23 bits; `a` as one of 11 bits beside y's 8 in 16-bit layers, as two in fp32 ones.  Groups'
+// sums are kept apart in fp32 and scaled once, so no weight is rounded.  An expert's rows come in units of 16 (fp32: 8);
+// experts' output rows go to scratch, and a combine adds them.  64 tokens of the Medium layer (h 5120, f 1536, 6 of 128,
+// skewed): 155 us against a floor of 36; 13 fp32 tokens of the long-sequence layer (h f 2048, 2 of 128, groups of 32): 54
+// against 5.  Some 10 instructions a product (unpacking for one or two tiles of rows, copies, the groups' scales) at 1.7 a
+// clock, as two blocks an SM do not cover their latencies, and five launches are the rest.  (tcgen05 would want the unpacked
+// weights in shared memory and its sums read back after each group, as a scale inside the operands would round them; it
+// would pay from some 32 rows an expert on, and is not built.)
 //
 // A warp's step is 16 outputs x 128 inputs.  The sum over inputs may run in any order, so lane (g, q) = (lane / 4, lane % 4)
 // takes for outputs g and g + 8 the G/4 consecutive inputs of each group that are contiguous in its 4-bit row: the weights
 // need no other layout than [output][input / 2].  Two nibbles of a word sit 16 bits apart as inputs i and i + 4, so for the
-// tensor cores eight activations go in as (0,4) (1,5) (2,6) (3,7); planes are stored in that order ("paired" below).
+// tensor cores eight activations go in as (0,4) (1,5) (2,6) (3,7); planes are stored in that order.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -39,10 +43,12 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kTile = 16;       // outputs of a warp
 constexpr int kStep = 128;      // inputs of a warp's step
-constexpr int kFewTokens = 8, kFewRows = 64;
-constexpr int kTurn = 2;         // steps between barriers of the many form
-constexpr int kStages = 4;       // turns of activations in shared memory
-constexpr int kPass = 16;        // rows of a unit of the many form
+constexpr int kFewTokens = 8, kFewRows = 64, kSeveralRows = 12;
+constexpr int kTurn = 4;         // steps between barriers of the many form
+constexpr int kStages = 2;       // turns of activations in shared memory (three: the same)
+// Rows of a unit of the many form.  With two planes a second tile of rows would take the registers that hide the latency
+// (13 tokens of the long-sequence layer: 92 us).
+template <int P> constexpr int kPass = P == 1 ? 16 : 8;
 constexpr int kFewBytes = 100 * 1024;  // shared memory for the few form's activations
 constexpr int kFewSteps = 128;         // of a warp: kFewBytes / (128 inputs x 2.25 bytes) / 8, and one more an expert
 // One token: blocks an SM, and steps of weights under way in a warp.  Large / Small layer, both kernels: 4, 1 and 4 46 / 14 us;
@@ -58,88 +64,14 @@ struct W4Mat {
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_bf16_first(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {  // c = a b
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-// Nibbles i and i + 4 of w as two bf16: 128 + nibble has the nibble as its last mantissa bits.
-__device__ __forceinline__ uint32_t nibble_pair(uint32_t w, int i) {
-  const uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), __floats2bfloat162_rn(136.f, 136.f));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-// The A operands of a word's two products: w0 of output g, w1 of output g + 8.
-__device__ __forceinline__ void unpack_word(uint32_t w0, uint32_t w1, uint32_t a[2][4]) {
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    a[half][0] = nibble_pair(w0, 2 * half);
-    a[half][1] = nibble_pair(w1, 2 * half);
-    a[half][2] = nibble_pair(w0, 2 * half + 1);
-    a[half][3] = nibble_pair(w1, 2 * half + 1);
-  }
-}
-// Place of input i of eight in the paired order.
-__device__ __forceinline__ int paired(int i) { return (i & ~7) | ((i & 3) << 1) | ((i >> 2) & 1); }
-
-template <int P>
-__device__ __forceinline__ void split_planes(float v, __nv_bfloat16* out) {
-  out[0] = __float2bfloat16_rn(v);
-#pragma unroll
-  for (int p = 1; p < P; ++p) {
-    v -= __bfloat162float(out[p - 1]);
-    out[p] = __float2bfloat16_rn(v);
-  }
-}
-
-// Eight consecutive activations as paired bf16 planes: from x as the caller has it, or from `a`'s paired planes.
 struct E4M3 { unsigned char v; };
-template <typename X> struct Acts;
-template <> struct Acts<__nv_bfloat16> {
-  static constexpr int kPlanes = 1;
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, uint32_t b[1][4]) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    b[0][0] = __byte_perm(u.x, u.z, 0x5410); b[0][1] = __byte_perm(u.x, u.z, 0x7632);
-    b[0][2] = __byte_perm(u.y, u.w, 0x5410); b[0][3] = __byte_perm(u.y, u.w, 0x7632);
-  }
-};
-template <> struct Acts<float> {
-  static constexpr int kPlanes = 3;
-  static __device__ __forceinline__ void load(const float* p, uint32_t b[3][4]) {
-    const float4 lo = __ldg(reinterpret_cast<const float4*>(p)), hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    const float f[2][4] = {{lo.x, lo.y, lo.z, lo.w}, {hi.x, hi.y, hi.z, hi.w}};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __nv_bfloat16 u[3], v[3];
-      split_planes<3>(f[0][i], u);
-      split_planes<3>(f[1][i], v);
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        b[k][i] = (uint32_t)__bfloat16_as_ushort(u[k]) | ((uint32_t)__bfloat16_as_ushort(v[k]) << 16);
-    }
-  }
-};
-template <> struct Acts<E4M3> {
-  static constexpr int kPlanes = 1;
-  static __device__ __forceinline__ void load(const E4M3* p, uint32_t b[1][4]) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // e4m3 values have 4 significant bits: exact in bf16
-      const uint32_t two = ((u.x >> (8 * i)) & 0xffu) | (((u.y >> (8 * i)) & 0xffu) << 8);
-      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
-      b[0][i] = pack_bf16x2(f.x, f.y);
-    }
-  }
-};
 
 // A lane's place in a matrix of one expert: byte offset of output g's row and this lane's quarter of a group, and offset of
 // its scales; output g + 8 lies `q8` and `s8` further.  32 bits suffice for an expert's matrix.
@@ -157,36 +89,6 @@ struct LanePlace {
   }
 };
 
-// A group's words (their A operands f) with two column tiles of activations, all planes.  One or two planes: one chain of
-// sums a tile.  Three (fp32): the small planes in a chain of their own, as the tensor core's sums round towards zero.
-template <int P, int G, typename LOAD>
-__device__ __forceinline__ void group_pair(const uint32_t (*f)[2][4], LOAD load, float part[2][4]) {
-  float low[2][4];
-#pragma unroll
-  for (int j = 0; j < G / 32; ++j)
-#pragma unroll
-    for (int p = P - 1; p >= 0; --p) {
-      const bool apart = P == 3 && p > 0, first = j == 0 && (apart ? p == P - 1 : P == 3 || p == P - 1);
-      uint4 u[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) u[t] = load(t, j, p);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float* to = apart ? low[t] : part[t];
-        if (first) mma_bf16_first(to, f[j][0], u[t].x, u[t].y);
-        else mma_bf16(to, f[j][0], u[t].x, u[t].y);
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) mma_bf16(apart ? low[t] : part[t], f[j][1], u[t].z, u[t].w);
-    }
-  if constexpr (P == 3) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) part[t][c] += low[t][c];
-  }
-}
-
 // Where the eight inputs number c of a step (16 of them) go: the word, and the lane quarter that reads it.
 template <int G>
 __device__ __forceinline__ void place_of(int c, int* word, int* quarter) {
@@ -196,8 +98,7 @@ __device__ __forceinline__ void place_of(int c, int* word, int* quarter) {
 
 // ------------------------------------------------------------------------------------ few rows
 
-// With one or two rows an expert the tensor cores would be fed mostly zeros, and making bf16 of the nibbles (11
-// instructions for 8) is what takes the time.  Here the nibbles stay integers: 8 inputs' nibbles become two words of signed
+// With one or two rows an expert the tensor cores would be fed mostly zeros, and the latency of their products is what takes the time.  Here the nibbles stay integers: 8 inputs' nibbles become two words of signed
 // bytes 16 * (nibble - 8) in three instructions, and dp4a adds their products with the activations.  Those are integers
 // too, of 16 bits (bf16 and e4m3 activations) or 24 (fp32), as P signed bytes, with one fp32 scale per 16 inputs: an
 // activation is off by at most 2^-16 (2^-24) of the largest of its 16, far below what the output's type can show.
@@ -629,31 +530,25 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS) w4_few_down_kernel(const 
 
 // ------------------------------------------------------------------------------------ many rows
 
-// What the products work through: units of an expert and up to kPass of its rows, and the rows by expert.
+// With operands n 2^-24 the sums start at -8 2^-24 times the sum of the row's activations in the group, which takes the 8 of
+// nibble - 8 off.  The tensor core aligns a subnormal's products as if it were the least normal number, so that their sums
+// lose some bits: measured, outputs are off by 4e-6 of their norm, far below a 16-bit output's own rounding (1.7e-3).  fp32
+// layers turn the nibbles into n - 8, normal numbers (four more instructions, exact): 2e-7.  The second nibble of a byte
+// comes times 16: the activations it meets (inputs 1, 3, 5, 7 of eight) are stored times 1/16.  f16 reaches from 2^15
+// down to steps of 2^-24: what is lost of an activation is below 2^-34 of the largest of the row's 128.
+//
+// What the products work through: units of an expert and up to `pass` of its rows, and the rows by expert.
 struct ManyPlan {
   int units, pad[3];
   int unit[1];  // units x (expert, first place in the rows' list, rows), then the list
 };
-__host__ __device__ __forceinline__ int most_units(int rows, int E) {  // an expert's last unit may be short
-  return (rows < E ? rows : E) + rows / kPass;
+__host__ __device__ __forceinline__ int most_units(int rows, int E, int pass) {  // an expert's last unit may be short
+  return (rows < E ? rows : E) + rows / pass;
 }
 
-// x [T, K] to paired bf16 planes [P][T][K]; block 0 makes the plan.  The place of a row in its expert's part of the list
-// is whichever its atomic gives it: a row is a column of its own in every product, and no result depends on which.
-template <typename X>
-__global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x, long long eights, __nv_bfloat16* __restrict__ out,
-                                                         const int* __restrict__ topk_idx, int rows, int E, ManyPlan* plan) {
-  constexpr int P = Acts<X>::kPlanes;
-  launch_dependents();
-  if (blockIdx.x > 0) {
-    const long long i = (long long)(blockIdx.x - 1) * 256 + threadIdx.x;
-    if (i >= eights) return;
-    uint32_t b[P][4];
-    Acts<X>::load(x + i * 8, b);
-#pragma unroll
-    for (int p = 0; p < P; ++p) reinterpret_cast<uint4*>(out)[p * eights + i] = make_uint4(b[p][0], b[p][1], b[p][2], b[p][3]);
-    return;
-  }
+// One block makes the plan.  The place of a row in its expert's part of the list is whichever its atomic gives it: a row is a
+// column of its own in every product, and no result depends on which.
+__device__ __forceinline__ void make_plan(const int* __restrict__ topk_idx, int rows, int E, int pass, ManyPlan* plan) {
   __shared__ int count[1024], start[1024];
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   for (int e = threadIdx.x; e < E; e += 256) count[e] = 0;
@@ -666,7 +561,7 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x
   if (warp == 0) {  // rows and units before each expert
     int before = 0, units = 0;
     for (int e0 = 0; e0 < E; e0 += kWarp) {
-      const int e = e0 + lane, c = e < E ? count[e] : 0, u = (c + kPass - 1) / kPass;
+      const int e = e0 + lane, c = e < E ? count[e] : 0, u = (c + pass - 1) / pass;
       int cs = c, us = u;
 #pragma unroll
       for (int o = 1; o < kWarp; o <<= 1) {
@@ -678,8 +573,8 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x
         for (int i = 0; i < u; ++i) {
           int* to = plan->unit + 3 * (units + us - u + i);
           to[0] = e;
-          to[1] = before + cs - c + i * kPass;
-          to[2] = min(c - i * kPass, kPass);
+          to[1] = before + cs - c + i * pass;
+          to[2] = min(c - i * pass, pass);
         }
       }
       before += __shfl_sync(0xffffffffu, cs, kWarp - 1);
@@ -688,38 +583,204 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(const X* __restrict__ x
     if (lane == 0) plan->units = units;
   }
   __syncthreads();
-  int* list = plan->unit + 3 * most_units(rows, E);
+  int* list = plan->unit + 3 * most_units(rows, E, pass);
   for (int r = threadIdx.x; r < rows; r += 256) {
     const int e = __ldg(topk_idx + r);
     if ((unsigned)e < (unsigned)E) list[atomicAdd(&start[e], 1)] = r;
   }
 }
 
+// Of a row and group: the scale of its activations, and where its sums start.
+struct BlockNote {
+  float scale, start;
+};
+// P planes of eight inputs each, in a word's order (0,4) (1,5) (2,6) (3,7).
+struct HalfRows {
+  uint4* plane;     // [rows][K / 8][P]
+  BlockNote* note;  // [rows][groups]
+};
+template <typename X> constexpr int kHalfPlanes = sizeof(X) == 4 ? 2 : 1;
+
+__device__ __forceinline__ void load8(const float* p, float* f) {
+  const float4 lo = *reinterpret_cast<const float4*>(p), hi = *(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = lo.x; f[1] = lo.y; f[2] = lo.z; f[3] = lo.w; f[4] = hi.x; f[5] = hi.y; f[6] = hi.z; f[7] = hi.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) {
+  unpack(*reinterpret_cast<const uint4*>(p), f, __nv_bfloat16());
+}
+__device__ __forceinline__ void load8(const E4M3* p, float* f) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((i < 2 ? u.x : u.y) >> (16 * (i & 1))), __NV_E4M3)));
+    f[2 * i] = v.x; f[2 * i + 1] = v.y;
+  }
+}
+
+// Rows [rows, K] of x or `a` to P planes: 16 threads a row's step.  plan: block 0 makes it.
+template <typename X, int P, int G>
+__global__ void __launch_bounds__(256) w4_planes_kernel(const X* x, const float* __restrict__ x_scale, int rows, int K, HalfRows out,
+                                                        const int* __restrict__ topk_idx, int slots, int E, ManyPlan* plan) {
+  launch_dependents();
+  wait_dependency();
+  if (plan != nullptr && blockIdx.x == 0) {
+    make_plan(topk_idx, slots, E, kPass<P>, plan);
+    return;
+  }
+  const int S = (K + kStep - 1) / kStep, block = blockIdx.x - (plan != nullptr ? 1 : 0);
+  const long long place = (long long)block * 16 + threadIdx.x / 16;
+  const int row = (int)(place / S), s = (int)(place % S), c = threadIdx.x % 16, k = s * kStep + c * 8;
+  const bool in = row < rows && k < K;
+  float v[8] = {}, scale = 0.f, inverse = 0.f;
+  if (in) load8(x + (size_t)row * K + k, v);
+  if constexpr (sizeof(X) == 1) {
+    scale = in ? __ldg(x_scale + (size_t)row * S + s) * 0x1p-6f : 0.f;
+    inverse = 0x1p6f;  // the largest is 448
+  } else {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    // a power of two that brings the largest to 2^14 or more and below 2^15
+    if (most >= 0x7f800000u) {
+      scale = __uint_as_float(0x7fc00000u);
+    } else if (__uint_as_float(most) >= 0x1p-90f) {
+      const int e = (int)(most >> 23) - 127 - 14;
+      scale = __uint_as_float((uint32_t)(127 + e) << 23);
+      inverse = __uint_as_float((uint32_t)(127 - e) << 23);
+    }
+  }
+  float total = 0.f;
+  uint4 w[P];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // inputs i and i + 4
+    const float at = i % 2 == 0 ? 1.f : 0.0625f;
+    float lo = inverse == 0.f ? 0.f : v[i] * (inverse * at), hi = inverse == 0.f ? 0.f : v[i + 4] * (inverse * at);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const __half2 two = __floats2half2_rn(lo, hi);
+      const float2 d = __half22float2(two);
+      lo -= d.x;
+      hi -= d.y;
+      total += (d.x + d.y) / at;
+      (&w[p].x)[i] = *reinterpret_cast<const uint32_t*>(&two);
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < G / 8; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (!in) return;
+#pragma unroll
+  for (int p = 0; p < P; ++p) out.plane[((size_t)row * K + k) / 8 * P + p] = w[p];
+  if (c % (G / 8) == 0) out.note[(size_t)row * ((K + G - 1) / G) + k / G] = BlockNote{scale, total * -0x1p-21f};
+}
+
 struct ManyArgs {
-  const __nv_bfloat16* x;  // paired planes [P][xrows][K]
-  const float* x_scale;
+  HalfRows x;
   const ManyPlan* plan;
-  int rows, k, xrows, E, K, N;  // row r of topk_idx reads x's row r / k (gate/up) or r (down: k = 1)
+  int rows, k, E, K, N;  // row r of topk_idx reads x's row r / k (gate/up) or r (down: k = 1)
   W4Mat mat[2];
-  void* out;               // gate/up: a's planes [PA][rows][N]; down: [rows, N] fp32
+  float* out;            // [rows, N]: a, or the outputs of the rows
 };
 
-// Blocks take turns at the items of a unit.  A warp has one tile of 16 outputs of one matrix (gate/up: half of the warps W1,
-// the other half W3), and every split-th step of it; a turn of the loop is kTurn steps.  With many items the tiles lie side
-// by side over the warps (split 1: 64 outputs of both matrices, or 128); with few, two warps share a tile's steps, so
-// that there are more and shorter items.  Which one follows from the number of units, known here alone: split 1
-// from one and a half items a block on (64 tokens of the Medium layer: 200 us, and 243 with 2; 13 fp32 ones of the
-// long-sequence layer: 87 and 71).
-template <int P, int PA, int G, bool GATEUP, bool SCALED, int SPLIT>
-__device__ __forceinline__ void many_items(const ManyArgs& a, uint4* stage, int* list, int* source) {
-  constexpr int MOST = GATEUP ? kWarps / 2 : kWarps, TILES = kPass / 8, VALUES = TILES * 4;
-  constexpr int STEP = TILES * 4 * 32 * P;  // 16-byte pieces of a step's activations: [row tile][word][plane][lane]
-  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, mat = warp / MOST;
-  const int S = (a.K + kStep - 1) / kStep, turns = (S + kTurn - 1) / kTurn;
-  constexpr int WIDE = MOST / SPLIT;
-  const int across = (a.N + WIDE * kTile - 1) / (WIDE * kTile), items = a.plan->units * across;
-  const int tile = warp % MOST % WIDE, part = warp % MOST / WIDE;
-  const int* rows_by_expert = a.plan->unit + 3 * most_units(a.rows, a.E);
+// Shared memory of one stage: a turn's activations, [step][row tile][word][plane][lane], and its notes, [group][row].
+template <int P> constexpr int kPlaneBytes = kTurn * (kPass<P> / 8) * 4 * P * 32 * 16;
+template <int P, int G> constexpr int kStageBytes = kPlaneBytes<P> + kTurn * (kStep / G) * kPass<P> * 8;
+
+// The nibbles i, i + 4 (and, times 16, i + 1, i + 5) of a word as two f16 n 2^-24; EXACT: n - 8 (1024 + n has n as its last
+// mantissa bits).
+template <bool EXACT>
+__device__ __forceinline__ void unpack_word(uint32_t w0, uint32_t w1, uint32_t f[2][4]) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = ((i % 2 == 0 ? w0 : w1) >> (8 * half)) & (i < 2 ? 0x000f000fu : 0x00f000f0u);
+      if constexpr (EXACT) {
+        const uint32_t n = u | 0x64006400u;
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&n), __float2half2_rn(i < 2 ? 1032.f : 1152.f));
+        f[half][i] = *reinterpret_cast<const uint32_t*>(&d);
+      } else {
+        f[half][i] = u;
+      }
+    }
+}
+
+// A step of a warp: the weights w, once they are used `load` fetches the next into their place.  TILES tiles of 8 rows; one
+// tile's sums go in two chains, of even and of odd words, so that a warp has four chains of products under way either way.
+template <int P, int G, int TILES, typename LOAD>
+__device__ __forceinline__ void many_step(IntWeights<G, 2>& w, const uint4* b, const float2* note, float (*acc)[kPass<P> / 8][4], LOAD load) {
+  constexpr bool EXACT = P == 2;
+#pragma unroll
+  for (int i = 0; i < kStep / G; ++i) {
+    constexpr int CHAINS = TILES == 2 || G > 32 ? 2 : 1;
+    float sum[2][CHAINS][4], low[2][CHAINS][4];  // low: of the second plane
+    float4 of[TILES];                            // scale and start of two rows
+#pragma unroll
+    for (int u = 0; u < TILES; ++u) of[u] = *reinterpret_cast<const float4*>(note + i * kPass<P> + u * 8);
+#pragma unroll
+    for (int u = 0; u < CHAINS; ++u)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          sum[m][u][v] = EXACT || u >= TILES ? 0.f : v % 2 == 0 ? of[u % TILES].y : of[u % TILES].w;
+          low[m][u][v] = 0.f;
+        }
+    float g[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) g[m][v] = __bfloat162float(w.s[m][v][i]) * (EXACT ? 1.f : 0x1p24f);
+#pragma unroll
+    for (int j = i * (G / 32); j < (i + 1) * (G / 32); ++j) {
+      uint32_t f[2][2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) unpack_word<EXACT>(w.w[m][0][j], w.w[m][1][j], f[m]);
+#pragma unroll
+      for (int u = 0; u < TILES; ++u) {
+        const int chain = TILES == 2 ? u : j % CHAINS;
+        const uint4 x = b[(u * 4 + j) * (P * 32)];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) mma_f16(sum[m][chain], f[m][0], x.x, x.y);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) mma_f16(sum[m][chain], f[m][1], x.z, x.w);
+        if constexpr (P == 2) {
+          const uint4 y = b[((u * 4 + j) * P + 1) * 32];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) mma_f16(low[m][chain], f[m][0], y.x, y.y);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) mma_f16(low[m][chain], f[m][1], y.z, y.w);
+        }
+      }
+    }
+    if (i == kStep / G - 1) load(w);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int u = 0; u < TILES; ++u)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float all = sum[m][u][v];
+          if constexpr (P == 2) all += low[m][u][v];
+          if constexpr (TILES < CHAINS) all += P == 2 ? sum[m][1][v] + low[m][1][v] : sum[m][1][v];
+          acc[m][u][v] = fmaf(all, g[m][v / 2] * (v % 2 == 0 ? of[u].x : of[u].z), acc[m][u][v]);
+        }
+  }
+}
+
+// Blocks take turns at the items of a unit.  A warp has two tiles of 16 outputs, which share their activations: the same
+// outputs of W1 and W3, or neighbours of W2.  SPLIT warps share a pair's steps, and add up at the end, so that there are
+// more and shorter items: 1 from an item a block on (13 tokens of the Small layer, 1.3 to 1.8 items a block: 77 us, and with 2
+// warps 80), 2 from a quarter on (64 tokens, 2 of 8 experts, h f 2048, 0.4 to 0.8: 60, with 1 69, with 4 70), else 4 (13
+// fp32 tokens of the long-sequence layer, 0.2 to 0.3: 54, with 2 62, with 1 87).
+template <int P, int G, bool GATEUP, int SPLIT>
+__device__ __forceinline__ void many_items(const ManyArgs& a, unsigned char* stages, int* list, int* source) {
+  constexpr int WIDE = kWarps / SPLIT, OUTS = WIDE * kTile * (GATEUP ? 1 : 2), GROUPS = kStep / G;
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, tile = warp % WIDE, part = warp / WIDE;
+  const int S = (a.K + kStep - 1) / kStep, turns = (S + kTurn - 1) / kTurn, groups = (a.K + G - 1) / G;
+  const int across = (a.N + OUTS - 1) / OUTS, items = a.plan->units * across;
+  const int* rows_by_expert = a.plan->unit + 3 * most_units(a.rows, a.E, kPass<P>);
   // an item's expert, number of rows and, in thread i, its i-th row: read an item ahead
   int e = 0, n = 0, r = 0;
   auto look = [&](int item) {
@@ -732,51 +793,64 @@ __device__ __forceinline__ void many_items(const ManyArgs& a, uint4* stage, int*
   look(blockIdx.x);
   const LanePlace<G> lanes(0, a.K, lane);  // strides, and this lane's place in the first tile
   // this thread's pieces of a turn's activations: the same eight inputs of rows APART apart
+  constexpr int ROWS = kPass<P>, APART = kWarps * 2 / kTurn, FILLS = ROWS / APART;
+  static_assert(FILLS * APART == ROWS && 8 % APART == 0, "the threads divide a turn evenly");
+  static_assert(kTurn * GROUPS * ROWS <= kWarps * 32, "a thread copies one note at most");
   const int c = threadIdx.x % (16 * kTurn), r0 = threadIdx.x / (16 * kTurn);
-  constexpr int APART = kWarps * 32 / (16 * kTurn), FILLS = kPass / APART;
   int word, quarter;
   place_of<G>(c % 16, &word, &quarter);
+  const uint32_t stage0 = ptx::smem_u32(stages), piece = ((c / 16 * (ROWS / 2) + word) * (P * 32) + r0 * 4 + quarter) * 16;
   const int c0 = (lane % 4) * 2;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    __syncthreads();  // the last item's list and stages have been read
+    __syncthreads();  // the last item's list and sums have been read
     if (threadIdx.x < n) {
       list[threadIdx.x] = r;
       source[threadIdx.x] = r / a.k;
     }
-    const int out0 = (item % across * WIDE + tile) * kTile, rows = n;
-    const bool live = out0 < a.N;
+    const int out0 = item % across * OUTS + tile * kTile * (GATEUP ? 1 : 2), rows = n;
+    const bool live = out0 < a.N;  // N is a multiple of 32
     const size_t row0 = (size_t)e * a.N + (live ? out0 : 0);
-    const unsigned char* q = a.mat[mat].q + row0 * (a.K / 2) + lanes.q + part * (kStep / 2);
-    const __nv_bfloat16* sc = a.mat[mat].s + row0 * ((a.K + G - 1) / G) + lanes.s + part * (kStep / G);
-    IntWeights<G, 1> w[2];
+    const unsigned char* q[2];
+    const __nv_bfloat16* sc[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const size_t at = row0 + (GATEUP ? 0 : m * kTile);
+      q[m] = a.mat[GATEUP ? m : 0].q + at * (a.K / 2) + lanes.q + part * (kStep / 2);
+      sc[m] = a.mat[GATEUP ? m : 0].s + at * groups + lanes.s + part * GROUPS;
+    }
+    IntWeights<G, 2> w[2];
     int k0 = part * kStep;  // of the weights to load next
-    auto load = [&](IntWeights<G, 1>& to) {
-      if (k0 < a.K) to.load(&q, &sc, lanes.q8, lanes.s8, k0 + lanes.k, k0, a.K);
+    auto load = [&](IntWeights<G, 2>& to) {
+      if (k0 < a.K) to.load(q, sc, lanes.q8, lanes.s8, k0 + lanes.k, k0, a.K);
       k0 += SPLIT * kStep;
-      q += SPLIT * (kStep / 2);
-      sc += SPLIT * (kStep / G);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        q[m] += SPLIT * (kStep / 2);
+        sc[m] += SPLIT * GROUPS;
+      }
     };
     load(w[0]);
     load(w[1]);
     __syncthreads();
     look(item + gridDim.x);
-    // a turn's activations: piece (row, eight) of plane p goes where lane (row % 8, quarter) reads it
-    const __nv_bfloat16* from[FILLS];
+    int from[FILLS];  // of the planes' pieces, and of the notes; below zero where there is no row
 #pragma unroll
-    for (int i = 0; i < FILLS; ++i)
-      from[i] = r0 + i * APART < rows ? a.x + (size_t)source[r0 + i * APART] * a.K + c * 8 : nullptr;
+    for (int i = 0; i < FILLS; ++i) from[i] = r0 + i * APART < rows ? (source[r0 + i * APART] * (a.K / 8) + c) * P : -1;
+    const int note_row = threadIdx.x % ROWS, note_group = threadIdx.x / ROWS;
+    const int note_from = note_row < rows && note_group < kTurn * GROUPS ? source[note_row] * groups + note_group : -1;
     auto fill = [&](int turn) {
-      const uint32_t to = ptx::smem_u32(stage + (turn % kStages * kTurn + c / 16) * STEP);
-      const int k = turn * kTurn * kStep;
+      const uint32_t to = stage0 + turn % kStages * kStageBytes<P, G>;
 #pragma unroll
       for (int i = 0; i < FILLS; ++i) {
-        const int row = r0 + i * APART;
-        const bool in = from[i] != nullptr && k + c * 8 < a.K;
-        const __nv_bfloat16* x = in ? from[i] + k : a.x;
+        if (i * APART >= 8 && rows <= 8) break;  // a tile that no product reads
+        const bool in = from[i] >= 0 && turn * kTurn * kStep + c * 8 < a.K;
+        const uint4* x = a.x.plane + (in ? from[i] + turn * (kTurn * 16 * P) : 0);
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-          ptx::cp_async_16(to + (((row / 8 * 4 + word) * P + p) * 32 + row % 8 * 4 + quarter) * 16, x + (size_t)p * a.xrows * a.K,
-                           in ? 16u : 0u);
+        for (int p = 0; p < P; ++p) ptx::cp_async_16(to + piece + (i * APART / 8 * 4 * P + p) * 512 + i * APART % 8 * 64, x + p, in ? 16u : 0u);
+      }
+      if (note_group < kTurn * GROUPS) {
+        const bool in = note_from >= 0 && turn * kTurn * GROUPS + note_group < groups;
+        ptx::cp_async_8(to + kPlaneBytes<P> + threadIdx.x * 8, a.x.note + (in ? note_from + turn * kTurn * GROUPS : 0), in ? 8u : 0u);
       }
     };
 #pragma unroll
@@ -784,18 +858,14 @@ __device__ __forceinline__ void many_items(const ManyArgs& a, uint4* stage, int*
       if (t < turns) fill(t);
       ptx::cp_async_commit();
     }
-    float acc[TILES][4];
-#pragma unroll
-    for (int t = 0; t < TILES; ++t)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[t][v] = 0.f;
+    float acc[2][ROWS / 8][4] = {};  // [tile of outputs][tile of rows]
     const int own = turns * kTurn / SPLIT;  // of a warp's steps, those beyond the inputs included
     int turn = 0;
     for (int o0 = 0; o0 < own; o0 += 2) {
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         if (o0 + d >= own) break;
-        if (d * SPLIT % kTurn == 0) {
+        if ((o0 + d) * SPLIT % kTurn == 0) {
           ptx::cp_async_wait<kStages - 2>();
           __syncthreads();  // the turn's activations are there, and the stage before it has been read by all
           if (turn + kStages - 1 < turns) fill(turn + kStages - 1);
@@ -804,74 +874,61 @@ __device__ __forceinline__ void many_items(const ManyArgs& a, uint4* stage, int*
         }
         const int s = (o0 + d) * SPLIT + part;
         if (s >= S) continue;
-        const uint4* b = stage + s % (kStages * kTurn) * STEP + lane;
-#pragma unroll
-        for (int i = 0; i < kStep / G; ++i) {
-          uint32_t f[G / 32][2][4];
-#pragma unroll
-          for (int j = 0; j < G / 32; ++j) unpack_word(w[d].w[0][0][i * (G / 32) + j], w[d].w[0][1][i * (G / 32) + j], f[j]);
-          const float g0 = __bfloat162float(w[d].s[0][0][i]), g1 = __bfloat162float(w[d].s[0][1][i]);
-          if (i == kStep / G - 1) load(w[d]);
-          static_assert(TILES == 2, "a pair of row tiles");
-          float sum[2][4];  // two chains of dependent products at once; the second may be of no rows
-          group_pair<P, G>(f, [&](int u, int j, int p) { return b[((u * 4 + i * (G / 32) + j) * P + p) * 32]; }, sum);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float x0 = 1.f, x1 = 1.f;
-            if constexpr (SCALED) {
-              const int row = u * 8 + c0;
-              x0 = row < rows ? __ldg(a.x_scale + (size_t)source[row] * S + s) : 0.f;
-              x1 = row + 1 < rows ? __ldg(a.x_scale + (size_t)source[row + 1] * S + s) : 0.f;
-            }
-            acc[u][0] = fmaf(sum[u][0], SCALED ? g0 * x0 : g0, acc[u][0]);
-            acc[u][1] = fmaf(sum[u][1], SCALED ? g0 * x1 : g0, acc[u][1]);
-            acc[u][2] = fmaf(sum[u][2], SCALED ? g1 * x0 : g1, acc[u][2]);
-            acc[u][3] = fmaf(sum[u][3], SCALED ? g1 * x1 : g1, acc[u][3]);
-          }
-        }
+        const unsigned char* stage = stages + (turn - 1) % kStages * kStageBytes<P, G>;
+        const uint4* b = reinterpret_cast<const uint4*>(stage) + s % kTurn * (ROWS / 2 * P * 32) + lane;
+        const float2* note = reinterpret_cast<const float2*>(stage + kPlaneBytes<P>) + s % kTurn * GROUPS * ROWS + c0;
+        if (ROWS > 8 && rows > 8) many_step<P, G, ROWS / 8>(w[d], b, note, acc, load);
+        else many_step<P, G, 1>(w[d], b, note, acc, load);
       }
     }
     ptx::cp_async_wait<0>();
-    __syncthreads();
-    // the parts' and the matrices' sums meet through shared memory: [warp][value][lane]
-    float* sums = reinterpret_cast<float*>(stage) + lane;
+    if constexpr (SPLIT > 1) {  // the parts' sums meet through shared memory: [value][warp][lane]
+      constexpr int TILES = ROWS / 8;
+      float* sums = reinterpret_cast<float*>(stages) + threadIdx.x;
+      __syncthreads();
+      if (part > 0) {
 #pragma unroll
-    for (int v = 0; v < VALUES; ++v) sums[(warp * VALUES + v) * 32] = acc[v / 4][v % 4];
-    __syncthreads();
-    if (mat == 0 && part == 0 && live) {
-#pragma unroll
-      for (int v = 0; v < VALUES; ++v) {
-        float y = acc[v / 4][v % 4], z = GATEUP ? sums[((MOST + tile) * VALUES + v) * 32] : 0.f;
-#pragma unroll
-        for (int i = 1; i < SPLIT; ++i) {
-          y += sums[((i * WIDE + tile) * VALUES + v) * 32];
-          if constexpr (GATEUP) z += sums[((MOST + i * WIDE + tile) * VALUES + v) * 32];
-        }
-        const int i = v / 4 * 8 + c0 + v % 2, o = out0 + lane / 4 + (v % 4 / 2) * 8;
-        if (i >= rows) continue;
-        if constexpr (GATEUP) {
-          __nv_bfloat16 plane[PA];
-          split_planes<PA>(y * sigmoidf_(y) * z, plane);
-#pragma unroll
-          for (int p = 0; p < PA; ++p)
-            static_cast<__nv_bfloat16*>(a.out)[((size_t)p * a.rows + list[i]) * a.N + paired(o)] = plane[p];
-        } else {
-          static_cast<float*>(a.out)[(size_t)list[i] * a.N + o] = y;
-        }
+        for (int v = 0; v < TILES * 8; ++v) sums[v * kWarps * 32] = acc[v % 2][v / 2 % TILES][v / (2 * TILES)];
       }
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int v = 0; v < TILES * 8; ++v)
+#pragma unroll
+          for (int i = 1; i < SPLIT; ++i) acc[v % 2][v / 2 % TILES][v / (2 * TILES)] += sums[(v * kWarps + i * WIDE) * 32];
+      }
+    }
+    if (part == 0 && live) {
+#pragma unroll
+      for (int u = 0; u < ROWS / 8; ++u)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int i = u * 8 + c0 + v % 2, o = out0 + lane / 4 + v / 2 * 8;
+          if (i >= rows) continue;
+          float* to = a.out + (size_t)list[i] * a.N + o;
+          if constexpr (GATEUP) {
+            to[0] = acc[0][u][v] * sigmoidf_(acc[0][u][v]) * acc[1][u][v];
+          } else {
+            to[0] = acc[0][u][v];
+            to[kTile] = acc[1][u][v];
+          }
+        }
     }
   }
 }
 
-template <int P, int PA, int G, bool GATEUP, bool SCALED>
+template <int P, int G, bool GATEUP>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_many_kernel(const __grid_constant__ ManyArgs a) {
-  extern __shared__ uint4 stage[];  // [stage][step of the turn][STEP]
-  __shared__ int list[kPass], source[kPass];
+  extern __shared__ __align__(16) unsigned char stages[];
+  __shared__ int list[kPass<P>], source[kPass<P>];
   launch_dependents();
   wait_dependency();
-  constexpr int OUTS = (GATEUP ? kWarps / 2 : kWarps) * kTile;
-  if (2 * a.plan->units * ((a.N + OUTS - 1) / OUTS) >= 3 * (int)gridDim.x) many_items<P, PA, G, GATEUP, SCALED, 1>(a, stage, list, source);
-  else many_items<P, PA, G, GATEUP, SCALED, 2>(a, stage, list, source);
+  constexpr int OUTS = kWarps * kTile * (GATEUP ? 1 : 2);
+  const int items = a.plan->units * ((a.N + OUTS - 1) / OUTS), blocks = gridDim.x;
+  const int split = items >= blocks ? 1 : 4 * items >= blocks ? 2 : 4;
+  if (split == 1) many_items<P, G, GATEUP, 1>(a, stages, list, source);
+  else if (split == 2) many_items<P, G, GATEUP, 2>(a, stages, list, source);
+  else many_items<P, G, GATEUP, 4>(a, stages, list, source);
 }
 
 // y[t] = sum_j topk_w[t,j] * rows[t*k+j], j ascending; a row of no expert counts as zeros.  The choices do not wait for the
@@ -962,7 +1019,6 @@ void launch_early(void (*kernel)(A), dim3 grid, int threads, size_t bytes, cudaS
   count_launch(st);
 }
 
-template <typename T> constexpr int kActPlanes = sizeof(T) == 2 ? 2 : 3;  // bf16 planes of `a`, many form
 template <typename T> constexpr int kIntPlanes = sizeof(T) == 2 ? 2 : 3;  // bytes of an activation, few form
 
 // Shared memory of `rows` rows of K activations in the few form.
@@ -1008,31 +1064,8 @@ void few(const W4Ffn& p, cudaStream_t st) {
   }
 }
 
-template <int P, int PA, int G, bool GATEUP, bool SCALED>
-void many_product(const ManyArgs& a, cudaStream_t st) {
-  constexpr int bytes = kStages * kTurn * (kPass / 8) * 4 * 32 * P * 16;
-  static_assert(bytes >= kWarps * kPass / 2 * 32 * 4, "the stages hold all warps' sums");
-  static bool ready[64] = {};
-  allow_shared(w4_many_kernel<P, PA, G, GATEUP, SCALED>, bytes, ready);
-  const long long items = (long long)most_units(a.rows, a.E) * (a.N / kTile), blocks = 2ll * num_sms();
-  launch_early(w4_many_kernel<P, PA, G, GATEUP, SCALED>, dim3((unsigned)(items < blocks ? items : blocks)), kWarps * 32, bytes, st, a);
-}
-
-template <typename X, typename T, int G>
-void many(const W4Ffn& p, cudaStream_t st) {
-  constexpr int PX = Acts<X>::kPlanes, PA = kActPlanes<T>;
-  const long long eights = (long long)p.T * p.h / 8;
-  ManyPlan* plan = static_cast<ManyPlan*>(p.plan);
-  w4_prepare_kernel<X><<<(unsigned)((eights + 255) / 256 + 1), 256, 0, st>>>(
-      static_cast<const X*>(p.x), eights, static_cast<__nv_bfloat16*>(p.x_planes), p.topk_idx, p.T * p.k, p.E, plan);
-  count_launch(st);
-  const ManyArgs up{static_cast<const __nv_bfloat16*>(p.x_planes), p.x_scale, plan, p.T * p.k, p.k, p.T, p.E, p.h, p.f,
-                    {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
-                     {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, p.a};
-  many_product<PX, PA, G, true, sizeof(X) == 1>(up, st);
-  const ManyArgs down{static_cast<const __nv_bfloat16*>(p.a), nullptr, plan, p.T * p.k, 1, p.T * p.k, p.E, p.f, p.h,
-                      {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.rows};
-  many_product<PA, PA, G, false, false>(down, st);
+template <typename T>
+void combine(const W4Ffn& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.T, (p.h / 4 + 255) / 256);
   cfg.blockDim = dim3(256);
@@ -1046,9 +1079,63 @@ void many(const W4Ffn& p, cudaStream_t st) {
   count_launch(st);
 }
 
+// Planes and notes of [rows, K] at `to`.
+template <int P>
+HalfRows half_rows(void* to, size_t rows, int K) {
+  unsigned char* b = static_cast<unsigned char*>(to);
+  return {reinterpret_cast<uint4*>(b), reinterpret_cast<BlockNote*>(b + rows * K * 2 * P)};
+}
+
+template <typename X, int P, int G>
+void to_planes(const X* x, const float* x_scale, int rows, int K, const HalfRows& out, const W4Ffn& p, ManyPlan* plan, cudaStream_t st) {
+  const long long steps = (long long)rows * ((K + kStep - 1) / kStep);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((steps + 15) / 16 + (plan != nullptr ? 1 : 0)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = plan != nullptr ? 0 : 1;  // the first launch follows whatever wrote x
+  cudaLaunchKernelEx(&cfg, w4_planes_kernel<X, P, G>, x, x_scale, rows, K, out, p.topk_idx, p.T * p.k, p.E, plan);
+  count_launch(st);
+}
+
+template <int P, int G, bool GATEUP>
+void many_product(const ManyArgs& a, cudaStream_t st) {
+  constexpr int stages = kStages * kStageBytes<P, G>, sums = kWarps * 16 * 32 * 4, bytes = stages > sums ? stages : sums;
+  static bool ready[64] = {};
+  allow_shared(w4_many_kernel<P, G, GATEUP>, bytes, ready);
+  const long long items = (long long)most_units(a.rows, a.E, kPass<P>) * (a.N / kTile), blocks = 2ll * num_sms();
+  launch_early(w4_many_kernel<P, G, GATEUP>, dim3((unsigned)(items < blocks ? items : blocks)), kWarps * 32, bytes, st, a);
+}
+
+template <typename X, typename T, int G>
+void many(const W4Ffn& p, cudaStream_t st) {
+  constexpr int P = kHalfPlanes<T>;
+  const int rows = p.T * p.k;
+  ManyPlan* plan = static_cast<ManyPlan*>(p.plan);
+  const HalfRows x = half_rows<P>(p.x_planes, p.T, p.h), act = half_rows<P>(p.a_planes, rows, p.f);
+  float* a = static_cast<float*>(p.a);
+  to_planes<X, P, G>(static_cast<const X*>(p.x), p.x_scale, p.T, p.h, x, p, plan, st);
+  const ManyArgs up{x, plan, rows, p.k, p.E, p.h, p.f,
+                    {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
+                     {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, a};
+  many_product<P, G, true>(up, st);
+  to_planes<float, P, G>(a, nullptr, rows, p.f, act, p, nullptr, st);
+  const ManyArgs down{act, plan, rows, 1, p.E, p.f, p.h,
+                      {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.rows};
+  many_product<P, G, false>(down, st);
+  combine<T>(p, st);
+}
+
 template <typename X, typename T, int G>
 void run_group(const W4Ffn& p, cudaStream_t st) {
-  const bool is_few = p.T <= kFewTokens && p.T * p.k <= kFewRows && few_bytes<T>(p.T, p.h) <= (size_t)kFewBytes &&
+  // Several tokens: the few form's second kernel does its rows one after another (8 rows of 2 tokens, h 1024, f 512: 12 us and
+  // in the many form 17; 12 rows of the Small layer: 35 and 33; 18 rows, h 832, f 1408: 46 and 36; 24 of the Small layer 59
+  // and 52).
+  const bool is_few = p.T <= kFewTokens && p.T * p.k <= (p.T == 1 ? kFewRows : kSeveralRows) && few_bytes<T>(p.T, p.h) <= (size_t)kFewBytes &&
                       few_bytes<T>(p.T * p.k, p.f) <= (size_t)kFewBytes;
   if (!is_few) many<X, T, G>(p, st);
   else if (p.T == 1) few<X, T, G, 1>(p, st);
@@ -1067,12 +1154,15 @@ void run(const W4Ffn& p, cudaStream_t st) {
 size_t w4_scratch(int dtype, long long T, long long k, int h, int E, int f, W4Scratch* at) {
   auto round = [](size_t b) { return (b + 255) & ~size_t(255); };
   W4Scratch s;
+  const size_t P = dtype == MOE_BF16 ? 1 : 2;
+  auto planes = [=](size_t rows, int K) { return round(rows * K * 2 * P + rows * ((K + 31) / 32) * sizeof(BlockNote)); };
   s.a = 0;
-  s.rows = s.a + round((size_t)T * k * f * 2 * (dtype == MOE_BF16 ? 2 : 3));
+  s.rows = s.a + round((size_t)T * k * f * sizeof(float));
   s.x_planes = s.rows + round((size_t)T * k * h * sizeof(float));
-  s.plan = s.x_planes + round((size_t)T * h * 2 * (dtype == MOE_BF16 ? 1 : 3));
+  s.a_planes = s.x_planes + planes(T, h);
+  s.plan = s.a_planes + planes(T * k, f);
   if (at != nullptr) *at = s;
-  return s.plan + round(16 + sizeof(int) * (3 * (size_t)most_units((int)(T * k), E) + T * k));
+  return s.plan + round(16 + sizeof(int) * (3 * (size_t)most_units((int)(T * k), E, P == 1 ? kPass<1> : kPass<2>) + T * k));
 }
 
 void launch_expert_ffn_w4(int dtype, const W4Ffn& p, cudaStream_t st) {
