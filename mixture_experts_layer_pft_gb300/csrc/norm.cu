@@ -117,20 +117,27 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* 
 #pragma unroll
       for (int i = 0; i < VN; i += 4) {
         const float4 g = load4(gamma + (size_t)v * VN + i);
-        f[u][i] *= rs * g.x; f[u][i + 1] *= rs * g.y; f[u][i + 2] *= rs * g.z; f[u][i + 3] *= rs * g.w;
+        f[u][i] *= g.x; f[u][i + 1] *= g.y; f[u][i + 2] *= g.z; f[u][i + 3] *= g.w;
       }
 #pragma unroll
       for (int i = 0; i < VN; ++i) amax = fmaxf(amax, fabsf(f[u][i]));
-      if (y != nullptr) reinterpret_cast<uint4*>(y)[row + v] = pack(f[u], T());
+      if (y != nullptr) {
+        float o[VN];
+#pragma unroll
+        for (int i = 0; i < VN; ++i) o[i] = f[u][i] * rs;
+        reinterpret_cast<uint4*>(y)[row + v] = pack(o, T());
+      }
     }
     if (q != nullptr) {
       // 128 columns are kQGroup / VN neighbouring lanes (tpr is a multiple of 32)
 #pragma unroll
       for (int o = kQGroup / VN / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const float scale = fmaxf(amax, 0x1p-100f) / 448.0f;
+      // rstd cancels in y / scale: without it a code has two roundings less that may push it over a tie
+      const float most = rs * amax, scale = fmaxf(most, 0x1p-100f) / 448.0f;
+      const float inv = most >= 0x1p-100f ? 448.0f / amax : rs * (448.0f * 0x1p100f);
       if (v < nvec) {
         if (v % (kQGroup / VN) == 0) q_scale[(size_t)t * groups + v / (kQGroup / VN)] = scale;
-        store_q<VN>(q + (row + v) * VN, f[u], 1.0f / scale);
+        store_q<VN>(q + (row + v) * VN, f[u], inv);
       }
     }
   }
