@@ -833,24 +833,24 @@ __device__ __forceinline__ void many_items(const ManyArgs& a, unsigned char* sta
     load(w[1]);
     __syncthreads();
     look(item + gridDim.x);
-    int from[FILLS];  // of the planes' pieces, and of the notes; below zero where there is no row
+    int from[FILLS];  // rows of x; below zero where there is none
 #pragma unroll
-    for (int i = 0; i < FILLS; ++i) from[i] = r0 + i * APART < rows ? (source[r0 + i * APART] * (a.K / 8) + c) * P : -1;
+    for (int i = 0; i < FILLS; ++i) from[i] = r0 + i * APART < rows ? source[r0 + i * APART] : -1;
     const int note_row = threadIdx.x % ROWS, note_group = threadIdx.x / ROWS;
-    const int note_from = note_row < rows && note_group < kTurn * GROUPS ? source[note_row] * groups + note_group : -1;
+    const int note_from = note_row < rows && note_group < kTurn * GROUPS ? source[note_row] : -1;
     auto fill = [&](int turn) {
       const uint32_t to = stage0 + turn % kStages * kStageBytes<P, G>;
 #pragma unroll
       for (int i = 0; i < FILLS; ++i) {
         if (i * APART >= 8 && rows <= 8) break;  // a tile that no product reads
         const bool in = from[i] >= 0 && turn * kTurn * kStep + c * 8 < a.K;
-        const uint4* x = a.x.plane + (in ? from[i] + turn * (kTurn * 16 * P) : 0);
+        const uint4* x = a.x.plane + (in ? ((size_t)from[i] * (a.K / 8) + turn * (kTurn * 16) + c) * P : 0);
 #pragma unroll
         for (int p = 0; p < P; ++p) ptx::cp_async_16(to + piece + (i * APART / 8 * 4 * P + p) * 512 + i * APART % 8 * 64, x + p, in ? 16u : 0u);
       }
       if (note_group < kTurn * GROUPS) {
         const bool in = note_from >= 0 && turn * kTurn * GROUPS + note_group < groups;
-        ptx::cp_async_8(to + kPlaneBytes<P> + threadIdx.x * 8, a.x.note + (in ? note_from + turn * kTurn * GROUPS : 0), in ? 8u : 0u);
+        ptx::cp_async_8(to + kPlaneBytes<P> + threadIdx.x * 8, a.x.note + (in ? (size_t)note_from * groups + turn * kTurn * GROUPS + note_group : 0), in ? 8u : 0u);
       }
     };
 #pragma unroll
