@@ -13,18 +13,23 @@
 // tensor cores in this place 86 us).  Small layer (h 2048, f 1408, 6 of 64): 14 us, of which the launches, the chain from
 // topk_idx to y and the host are most.
 //
-// "Many": tensor cores with 16 outputs as M and token rows as N.  A nibble n masked out of its word and read as f16 is the
-// subnormal n 2^-24, exactly: eight nibbles are operands after five instructions (bf16 operands would take eleven; e4m3
-// ones, which n 2^-9 would be as easily, three, but mma.sync does 0.28 of those a clock and SM once they change).
+// "Many": tensor cores with 16 outputs as M and token rows as N.  A nibble n masked into the mantissa of an f16 1024 is
+// 1024 + n, and n - 8 after a subtraction, exactly: eight nibbles are operands after nine instructions (in bf16 eleven).
 // Activations go in as planes of f16 over one scale per row and step, which is a power of two: x in e4m3 and bf16 as one,
-// exactly; x in fp32 as two, of 23 bits; `a` as one of 11 bits beside y's 8 in 16-bit layers, as two in fp32 ones.  Groups'
-// sums are kept apart in fp32 and scaled once, so no weight is rounded.  An expert's rows come in units of 16 (fp32: 8);
-// experts' output rows go to scratch, and a combine adds them.  64 tokens of the Medium layer (h 5120, f 1536, 6 of 128,
-// skewed): 155 us against a floor of 36; 13 fp32 tokens of the long-sequence layer (h f 2048, 2 of 128, groups of 32): 54
-// against 5.  Some 10 instructions a product (unpacking for one or two tiles of rows, copies, the groups' scales) at 1.7 a
-// clock, as two blocks an SM do not cover their latencies, and five launches are the rest.  (tcgen05 would want the unpacked
+// exactly; x in fp32 as two, of 23 bits; `a` as one of 11 bits beside y's 8 in 16-bit layers, as two in fp32 ones (bf16
+// planes take one more each).  Groups' sums are kept apart in fp32 and scaled once, so no weight is rounded.  An expert's
+// rows come in units of 16 (fp32: 8); experts' output rows go to scratch, and a combine adds them.  64 tokens of the Medium
+// layer (h 5120, f 1536, 6 of 128, skewed): 176 to 183 us against a floor of 36 (with bf16 operands 213); 13 fp32 tokens of
+// the long-sequence layer (h f 2048, 2 of 128, groups of 32): 53 against 5 (70).  Unpacking for one or two tiles of rows,
+// copies and the groups' scales, some 12 instructions a product at 1.7 a clock, as two blocks an SM do not cover their
+// latencies, and five launches are the rest.
+//
+// Other operands: n alone is the subnormal f16 n 2^-24, with the 8 taken off where a group's sums start: five instructions,
+// 155 to 163 us, but the tensor core aligns its products as if n were 1024, and what is lost of the sums (4e-6 of the
+// outputs' norm) grows with the largest activation, also where it meets weights of zero.  e4m3 operands (n 2^-9, three
+// instructions): 288 us, mma.sync does 0.28 of those a clock and SM once they change.  tcgen05 would want the unpacked
 // weights in shared memory and its sums read back after each group, as a scale inside the operands would round them; it
-// would pay from some 32 rows an expert on, and is not built.)
+// would pay from some 32 rows an expert on, and is not built.
 //
 // A warp's step is 16 outputs x 128 inputs.  The sum over inputs may run in any order, so lane (g, q) = (lane / 4, lane % 4)
 // takes for outputs g and g + 8 the G/4 consecutive inputs of each group that are contiguous in its 4-bit row: the weights
@@ -530,12 +535,9 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS) w4_few_down_kernel(const 
 
 // ------------------------------------------------------------------------------------ many rows
 
-// With operands n 2^-24 the sums start at -8 2^-24 times the sum of the row's activations in the group, which takes the 8 of
-// nibble - 8 off.  The tensor core aligns a subnormal's products as if it were the least normal number, so that their sums
-// lose some bits: measured, outputs are off by 4e-6 of their norm, far below a 16-bit output's own rounding (1.7e-3).  fp32
-// layers turn the nibbles into n - 8, normal numbers (four more instructions, exact): 2e-7.  The second nibble of a byte
-// comes times 16: the activations it meets (inputs 1, 3, 5, 7 of eight) are stored times 1/16.  f16 reaches from 2^15
-// down to steps of 2^-24: what is lost of an activation is below 2^-34 of the largest of the row's 128.
+// The second nibble of a byte comes times 16 (16 (n - 8) is exact as well): the activations it meets, inputs 1, 3, 5, 7 of
+// eight, are stored times 1/16.  f16 reaches from 2^15 down to steps of 2^-24: what is lost of an activation is below 2^-34
+// of the largest of the row's 128.
 //
 // What the products work through: units of an expert and up to `pass` of its rows, and the rows by expert.
 struct ManyPlan {
@@ -590,14 +592,10 @@ __device__ __forceinline__ void make_plan(const int* __restrict__ topk_idx, int 
   }
 }
 
-// Of a row and group: the scale of its activations, and where its sums start.
-struct BlockNote {
-  float scale, start;
-};
 // P planes of eight inputs each, in a word's order (0,4) (1,5) (2,6) (3,7).
 struct HalfRows {
-  uint4* plane;     // [rows][K / 8][P]
-  BlockNote* note;  // [rows][groups]
+  uint4* plane;  // [rows][K / 8][P]
+  float* scale;  // [rows][steps]
 };
 template <typename X> constexpr int kHalfPlanes = sizeof(X) == 4 ? 2 : 1;
 
@@ -618,7 +616,7 @@ __device__ __forceinline__ void load8(const E4M3* p, float* f) {
 }
 
 // Rows [rows, K] of x or `a` to P planes: 16 threads a row's step.  plan: block 0 makes it.
-template <typename X, int P, int G>
+template <typename X, int P>
 __global__ void __launch_bounds__(256) w4_planes_kernel(const X* x, const float* __restrict__ x_scale, int rows, int K, HalfRows out,
                                                         const int* __restrict__ topk_idx, int slots, int E, ManyPlan* plan) {
   launch_dependents();
@@ -651,7 +649,6 @@ __global__ void __launch_bounds__(256) w4_planes_kernel(const X* x, const float*
       inverse = __uint_as_float((uint32_t)(127 - e) << 23);
     }
   }
-  float total = 0.f;
   uint4 w[P];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // inputs i and i + 4
@@ -663,16 +660,13 @@ __global__ void __launch_bounds__(256) w4_planes_kernel(const X* x, const float*
       const float2 d = __half22float2(two);
       lo -= d.x;
       hi -= d.y;
-      total += (d.x + d.y) / at;
       (&w[p].x)[i] = *reinterpret_cast<const uint32_t*>(&two);
     }
   }
-#pragma unroll
-  for (int o = 1; o < G / 8; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (!in) return;
 #pragma unroll
   for (int p = 0; p < P; ++p) out.plane[((size_t)row * K + k) / 8 * P + p] = w[p];
-  if (c % (G / 8) == 0) out.note[(size_t)row * ((K + G - 1) / G) + k / G] = BlockNote{scale, total * -0x1p-21f};
+  if (c == 0) out.scale[(size_t)row * S + s] = scale;
 }
 
 struct ManyArgs {
@@ -683,60 +677,50 @@ struct ManyArgs {
   float* out;            // [rows, N]: a, or the outputs of the rows
 };
 
-// Shared memory of one stage: a turn's activations, [step][row tile][word][plane][lane], and its notes, [group][row].
+// Shared memory of one stage: a turn's activations, [step][row tile][word][plane][lane], and their scales, [step][row].
 template <int P> constexpr int kPlaneBytes = kTurn * (kPass<P> / 8) * 4 * P * 32 * 16;
-template <int P, int G> constexpr int kStageBytes = kPlaneBytes<P> + kTurn * (kStep / G) * kPass<P> * 8;
+template <int P> constexpr int kStageBytes = kPlaneBytes<P> + kTurn * kPass<P> * 4;
 
-// The nibbles i, i + 4 (and, times 16, i + 1, i + 5) of a word as two f16 n 2^-24; EXACT: n - 8 (1024 + n has n as its last
-// mantissa bits).
-template <bool EXACT>
+// The A operands of a word's two products, w0 of output g, w1 of output g + 8: n - 8 of the nibbles i and i + 4 as two f16
+// (1024 + n has n as its last mantissa bits), and 16 (n - 8) of the next two.
 __device__ __forceinline__ void unpack_word(uint32_t w0, uint32_t w1, uint32_t f[2][4]) {
 #pragma unroll
   for (int half = 0; half < 2; ++half)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t u = ((i % 2 == 0 ? w0 : w1) >> (8 * half)) & (i < 2 ? 0x000f000fu : 0x00f000f0u);
-      if constexpr (EXACT) {
-        const uint32_t n = u | 0x64006400u;
-        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&n), __float2half2_rn(i < 2 ? 1032.f : 1152.f));
-        f[half][i] = *reinterpret_cast<const uint32_t*>(&d);
-      } else {
-        f[half][i] = u;
-      }
+      const uint32_t n = (((i % 2 == 0 ? w0 : w1) >> (8 * half)) & (i < 2 ? 0x000f000fu : 0x00f000f0u)) | 0x64006400u;
+      const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&n), __float2half2_rn(i < 2 ? 1032.f : 1152.f));
+      f[half][i] = *reinterpret_cast<const uint32_t*>(&d);
     }
 }
 
 // A step of a warp: the weights w, once they are used `load` fetches the next into their place.  TILES tiles of 8 rows; one
 // tile's sums go in two chains, of even and of odd words, so that a warp has four chains of products under way either way.
 template <int P, int G, int TILES, typename LOAD>
-__device__ __forceinline__ void many_step(IntWeights<G, 2>& w, const uint4* b, const float2* note, float (*acc)[kPass<P> / 8][4], LOAD load) {
-  constexpr bool EXACT = P == 2;
+__device__ __forceinline__ void many_step(IntWeights<G, 2>& w, const uint4* b, const float* scale, float (*acc)[kPass<P> / 8][4], LOAD load) {
+  float2 of[TILES];  // the scales of two rows
+#pragma unroll
+  for (int u = 0; u < TILES; ++u) of[u] = *reinterpret_cast<const float2*>(scale + u * 8);
 #pragma unroll
   for (int i = 0; i < kStep / G; ++i) {
     constexpr int CHAINS = TILES == 2 || G > 32 ? 2 : 1;
     float sum[2][CHAINS][4], low[2][CHAINS][4];  // low: of the second plane
-    float4 of[TILES];                            // scale and start of two rows
-#pragma unroll
-    for (int u = 0; u < TILES; ++u) of[u] = *reinterpret_cast<const float4*>(note + i * kPass<P> + u * 8);
 #pragma unroll
     for (int u = 0; u < CHAINS; ++u)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          sum[m][u][v] = EXACT || u >= TILES ? 0.f : v % 2 == 0 ? of[u % TILES].y : of[u % TILES].w;
-          low[m][u][v] = 0.f;
-        }
+        for (int v = 0; v < 4; ++v) sum[m][u][v] = low[m][u][v] = 0.f;
     float g[2][2];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) g[m][v] = __bfloat162float(w.s[m][v][i]) * (EXACT ? 1.f : 0x1p24f);
+      for (int v = 0; v < 2; ++v) g[m][v] = __bfloat162float(w.s[m][v][i]);
 #pragma unroll
     for (int j = i * (G / 32); j < (i + 1) * (G / 32); ++j) {
       uint32_t f[2][2][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) unpack_word<EXACT>(w.w[m][0][j], w.w[m][1][j], f[m]);
+      for (int m = 0; m < 2; ++m) unpack_word(w.w[m][0][j], w.w[m][1][j], f[m]);
 #pragma unroll
       for (int u = 0; u < TILES; ++u) {
         const int chain = TILES == 2 ? u : j % CHAINS;
@@ -764,7 +748,7 @@ __device__ __forceinline__ void many_step(IntWeights<G, 2>& w, const uint4* b, c
           float all = sum[m][u][v];
           if constexpr (P == 2) all += low[m][u][v];
           if constexpr (TILES < CHAINS) all += P == 2 ? sum[m][1][v] + low[m][1][v] : sum[m][1][v];
-          acc[m][u][v] = fmaf(all, g[m][v / 2] * (v % 2 == 0 ? of[u].x : of[u].z), acc[m][u][v]);
+          acc[m][u][v] = fmaf(all, g[m][v / 2] * (v % 2 == 0 ? of[u].x : of[u].y), acc[m][u][v]);
         }
   }
 }
@@ -795,7 +779,7 @@ __device__ __forceinline__ void many_items(const ManyArgs& a, unsigned char* sta
   // this thread's pieces of a turn's activations: the same eight inputs of rows APART apart
   constexpr int ROWS = kPass<P>, APART = kWarps * 2 / kTurn, FILLS = ROWS / APART;
   static_assert(FILLS * APART == ROWS && 8 % APART == 0, "the threads divide a turn evenly");
-  static_assert(kTurn * GROUPS * ROWS <= kWarps * 32, "a thread copies one note at most");
+  static_assert(kTurn * ROWS <= kWarps * 32, "a thread copies one scale at most");
   const int c = threadIdx.x % (16 * kTurn), r0 = threadIdx.x / (16 * kTurn);
   int word, quarter;
   place_of<G>(c % 16, &word, &quarter);
@@ -836,10 +820,10 @@ __device__ __forceinline__ void many_items(const ManyArgs& a, unsigned char* sta
     int from[FILLS];  // rows of x; below zero where there is none
 #pragma unroll
     for (int i = 0; i < FILLS; ++i) from[i] = r0 + i * APART < rows ? source[r0 + i * APART] : -1;
-    const int note_row = threadIdx.x % ROWS, note_group = threadIdx.x / ROWS;
-    const int note_from = note_row < rows && note_group < kTurn * GROUPS ? source[note_row] : -1;
+    const int scale_step = threadIdx.x / ROWS;
+    const int scale_from = scale_step < kTurn && threadIdx.x % ROWS < rows ? source[threadIdx.x % ROWS] : -1;
     auto fill = [&](int turn) {
-      const uint32_t to = stage0 + turn % kStages * kStageBytes<P, G>;
+      const uint32_t to = stage0 + turn % kStages * kStageBytes<P>;
 #pragma unroll
       for (int i = 0; i < FILLS; ++i) {
         if (i * APART >= 8 && rows <= 8) break;  // a tile that no product reads
@@ -848,9 +832,10 @@ __device__ __forceinline__ void many_items(const ManyArgs& a, unsigned char* sta
 #pragma unroll
         for (int p = 0; p < P; ++p) ptx::cp_async_16(to + piece + (i * APART / 8 * 4 * P + p) * 512 + i * APART % 8 * 64, x + p, in ? 16u : 0u);
       }
-      if (note_group < kTurn * GROUPS) {
-        const bool in = note_from >= 0 && turn * kTurn * GROUPS + note_group < groups;
-        ptx::cp_async_8(to + kPlaneBytes<P> + threadIdx.x * 8, a.x.note + (in ? (size_t)note_from * groups + turn * kTurn * GROUPS + note_group : 0), in ? 8u : 0u);
+      if (scale_step < kTurn) {
+        const bool in = scale_from >= 0 && turn * kTurn + scale_step < S;
+        ptx::cp_async_4(to + kPlaneBytes<P> + threadIdx.x * 4, a.x.scale + (in ? (size_t)scale_from * S + turn * kTurn + scale_step : 0),
+                        in ? 4u : 0u);
       }
     };
 #pragma unroll
@@ -874,11 +859,11 @@ __device__ __forceinline__ void many_items(const ManyArgs& a, unsigned char* sta
         }
         const int s = (o0 + d) * SPLIT + part;
         if (s >= S) continue;
-        const unsigned char* stage = stages + (turn - 1) % kStages * kStageBytes<P, G>;
+        const unsigned char* stage = stages + (turn - 1) % kStages * kStageBytes<P>;
         const uint4* b = reinterpret_cast<const uint4*>(stage) + s % kTurn * (ROWS / 2 * P * 32) + lane;
-        const float2* note = reinterpret_cast<const float2*>(stage + kPlaneBytes<P>) + s % kTurn * GROUPS * ROWS + c0;
-        if (ROWS > 8 && rows > 8) many_step<P, G, ROWS / 8>(w[d], b, note, acc, load);
-        else many_step<P, G, 1>(w[d], b, note, acc, load);
+        const float* scale = reinterpret_cast<const float*>(stage + kPlaneBytes<P>) + s % kTurn * ROWS + c0;
+        if (ROWS > 8 && rows > 8) many_step<P, G, ROWS / 8>(w[d], b, scale, acc, load);
+        else many_step<P, G, 1>(w[d], b, scale, acc, load);
       }
     }
     ptx::cp_async_wait<0>();
@@ -1079,14 +1064,14 @@ void combine(const W4Ffn& p, cudaStream_t st) {
   count_launch(st);
 }
 
-// Planes and notes of [rows, K] at `to`.
+// Planes and scales of [rows, K] at `to`.
 template <int P>
 HalfRows half_rows(void* to, size_t rows, int K) {
   unsigned char* b = static_cast<unsigned char*>(to);
-  return {reinterpret_cast<uint4*>(b), reinterpret_cast<BlockNote*>(b + rows * K * 2 * P)};
+  return {reinterpret_cast<uint4*>(b), reinterpret_cast<float*>(b + rows * K * 2 * P)};
 }
 
-template <typename X, int P, int G>
+template <typename X, int P>
 void to_planes(const X* x, const float* x_scale, int rows, int K, const HalfRows& out, const W4Ffn& p, ManyPlan* plan, cudaStream_t st) {
   const long long steps = (long long)rows * ((K + kStep - 1) / kStep);
   cudaLaunchConfig_t cfg{};
@@ -1098,13 +1083,13 @@ void to_planes(const X* x, const float* x_scale, int rows, int K, const HalfRows
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = plan != nullptr ? 0 : 1;  // the first launch follows whatever wrote x
-  cudaLaunchKernelEx(&cfg, w4_planes_kernel<X, P, G>, x, x_scale, rows, K, out, p.topk_idx, p.T * p.k, p.E, plan);
+  cudaLaunchKernelEx(&cfg, w4_planes_kernel<X, P>, x, x_scale, rows, K, out, p.topk_idx, p.T * p.k, p.E, plan);
   count_launch(st);
 }
 
 template <int P, int G, bool GATEUP>
 void many_product(const ManyArgs& a, cudaStream_t st) {
-  constexpr int stages = kStages * kStageBytes<P, G>, sums = kWarps * 16 * 32 * 4, bytes = stages > sums ? stages : sums;
+  constexpr int stages = kStages * kStageBytes<P>, sums = kWarps * 16 * 32 * 4, bytes = stages > sums ? stages : sums;
   static bool ready[64] = {};
   allow_shared(w4_many_kernel<P, G, GATEUP>, bytes, ready);
   const long long items = (long long)most_units(a.rows, a.E, kPass<P>) * (a.N / kTile), blocks = 2ll * num_sms();
@@ -1118,12 +1103,12 @@ void many(const W4Ffn& p, cudaStream_t st) {
   ManyPlan* plan = static_cast<ManyPlan*>(p.plan);
   const HalfRows x = half_rows<P>(p.x_planes, p.T, p.h), act = half_rows<P>(p.a_planes, rows, p.f);
   float* a = static_cast<float*>(p.a);
-  to_planes<X, P, G>(static_cast<const X*>(p.x), p.x_scale, p.T, p.h, x, p, plan, st);
+  to_planes<X, P>(static_cast<const X*>(p.x), p.x_scale, p.T, p.h, x, p, plan, st);
   const ManyArgs up{x, plan, rows, p.k, p.E, p.h, p.f,
                     {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
                      {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, a};
   many_product<P, G, true>(up, st);
-  to_planes<float, P, G>(a, nullptr, rows, p.f, act, p, nullptr, st);
+  to_planes<float, P>(a, nullptr, rows, p.f, act, p, nullptr, st);
   const ManyArgs down{act, plan, rows, 1, p.E, p.f, p.h,
                       {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, p.rows};
   many_product<P, G, false>(down, st);
@@ -1155,7 +1140,7 @@ size_t w4_scratch(int dtype, long long T, long long k, int h, int E, int f, W4Sc
   auto round = [](size_t b) { return (b + 255) & ~size_t(255); };
   W4Scratch s;
   const size_t P = dtype == MOE_BF16 ? 1 : 2;
-  auto planes = [=](size_t rows, int K) { return round(rows * K * 2 * P + rows * ((K + 31) / 32) * sizeof(BlockNote)); };
+  auto planes = [=](size_t rows, int K) { return round(rows * K * 2 * P + rows * ((K + kStep - 1) / kStep) * sizeof(float)); };
   s.a = 0;
   s.rows = s.a + round((size_t)T * k * f * sizeof(float));
   s.x_planes = s.rows + round((size_t)T * k * h * sizeof(float));

@@ -177,3 +177,58 @@ def test_captured_and_repeatable(B):
     assert torch.equal(y, want)
     empty = torch.zeros(0, 256, dtype=torch.bfloat16, device="cuda")
     layer.run(B, empty, None, idx[:0], w[:0], torch.bfloat16)
+
+
+@pytest.mark.parametrize("h,f", [(32, 32), (64, 96), (160, 224), (1056, 352), (2048, 192)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kind", ["bf16", "q8", "f32"])
+def test_twelve_rows(B, h, f, group, kind):
+    check(B, Layer(B, 6, h, f, group, DT[kind]), 4, 3, kind, seed=5)
+
+
+@pytest.mark.parametrize("E,T,k,h,f", [(40, 60, 4, 128, 2048), (40, 60, 4, 2048, 128), (24, 40, 2, 320, 1056), (3, 64, 1, 96, 64)])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("kind", ["bf16", "q8", "f32"])
+def test_many_and_few_items(B, E, T, k, h, f, group, kind):
+    check(B, Layer(B, E, h, f, group, DT[kind]), T, k, kind, seed=7)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_many_rows_do_not_see_one_another(B, kind):
+    layer = Layer(B, 4, 160, 96, 32, DT[kind])
+    x, _, _ = activations(21, 160, kind, 8)
+    idx, w = routing(21, 4, 2, 8)
+    clean = layer.run(B, x, None, idx, w, DT[kind])
+    bad = x.clone()
+    bad[2] = float("nan")
+    bad[4, 7] = float("inf")
+    y = layer.run(B, bad, None, idx, w, DT[kind])
+    keep = [t for t in range(21) if t not in (2, 4)]
+    assert torch.equal(y[keep], clean[keep])
+    assert torch.isnan(y[2]).all()
+
+
+def test_bad_experts_among_many_rows(B):
+    layer = Layer(B, 8, 64, 64, 32, torch.bfloat16)
+    idx = routing(30, 8, 2, 9)[0]
+    idx[1, 0], idx[2, 1], idx[3, 0], idx[3, 1] = -1, 8, 2 ** 31 - 1, -2 ** 31
+    y = check(B, layer, 30, 2, "bf16", idx=idx, status=B.MOE_STATUS_BAD_INDEX)
+    assert (y[3] == 0).all()
+
+
+@pytest.mark.parametrize("T,k", [(1, 2), (4, 3), (20, 2)])
+def test_a_large_value_that_meets_zero_weights(B, T, k):
+    """An input 2000 times the others whose weights are zero in every expert: what the others add is not lost beside it."""
+    layer = Layer(B, 4, 128, 64, 128, torch.bfloat16)
+    for i in (0, 1):
+        q = layer.mats[i][0]
+        q[:, :, 4] = (q[:, :, 4] & 0xF0) | 8  # the nibble of input 8
+        layer.dense[i] = O.weights_w4(q.cpu().numpy(), layer.mats[i][1].float().cpu().numpy(), 128)
+    x, _, _ = activations(T, 128, "bf16", 3)
+    x[:, 8] = 2000.0
+    idx, w = routing(T, 4, k, 3)
+    y = layer.run(B, x, None, idx, w, torch.bfloat16)
+    want, A, _ = O.expert_ffn_w4(np64(x), idx.cpu().numpy(), np64(w), *layer.dense)
+    # x is off by at most 2^-16 of 2000 (0.03 beside values of 1) in 16 of 128 inputs, a by 2^-8, y by 2^-8: an eighth of the
+    # row's largest output holds the sum of these for a dot product of 128 terms
+    assert np.abs(np64(y) - want).max() <= np.abs(want).max() / 8
