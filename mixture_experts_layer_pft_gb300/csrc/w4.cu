@@ -7,8 +7,8 @@
 // more than multiplying them.  Measured on this GPU, instructions a clock and SM: dp4a, LOP3, IMAD, I2F and bf16x2 FMA 1.9
 // each, mma.sync bf16 16x8x16 0.50, mma.sync s8 16x8x32 0.06.  Two forms follow from that.
 //
-// "Few" (one token, or up to 8 and 12 rows, whose activations fit in shared memory): integers through dp4a, see below.  Two launches:
-// the first writes `a`, the second adds each token's outputs over its experts in registers; it starts early and has its
+// "Few" (one token, or up to 8 and 12 rows, whose activations fit in shared memory): integers through dp4a, see below.
+// Two launches: the first writes `a`, the second adds each token's outputs over its experts in registers; it starts early and has its
 // first weights under way while the first still runs.  Large layer, one token in 8 bits: 46 us (58% of the floor's rate;
 // tensor cores in this place 86 us).  Small layer (h 2048, f 1408, 6 of 64): 14 us, of which the launches, the chain from
 // topk_idx to y and the host are most.
@@ -19,9 +19,9 @@
 // exactly; x in fp32 as two, of 23 bits; `a` as one of 11 bits beside y's 8 in 16-bit layers, as two in fp32 ones (bf16
 // planes take one more each).  Groups' sums are kept apart in fp32 and scaled once, so no weight is rounded.  An expert's
 // rows come in units of 16 (fp32: 8); experts' output rows go to scratch, and a combine adds them.  64 tokens of the Medium
-// layer (h 5120, f 1536, 6 of 128, skewed): 176 to 183 us against a floor of 36 (with bf16 operands 213); 13 fp32 tokens of
+// layer (h 5120, f 1536, 6 of 128, skewed): 171 to 183 us against a floor of 36 (with bf16 operands 213); 13 fp32 tokens of
 // the long-sequence layer (h f 2048, 2 of 128, groups of 32): 53 against 5 (70).  Unpacking for one or two tiles of rows,
-// copies and the groups' scales, some 12 instructions a product at 1.7 a clock, as two blocks an SM do not cover their
+// copies and the groups' scales, some 12 instructions a product at 2 a clock, as two blocks an SM do not cover their
 // latencies, and five launches are the rest.
 //
 // Other operands: n alone is the subnormal f16 n 2^-24, with the 8 taken off where a group's sums start: five instructions,
@@ -103,8 +103,9 @@ __device__ __forceinline__ void place_of(int c, int* word, int* quarter) {
 
 // ------------------------------------------------------------------------------------ few rows
 
-// With one or two rows an expert the tensor cores would be fed mostly zeros, and the latency of their products is what takes the time.  Here the nibbles stay integers: 8 inputs' nibbles become two words of signed
-// bytes 16 * (nibble - 8) in three instructions, and dp4a adds their products with the activations.  Those are integers
+// With one or two rows an expert the tensor cores would be fed mostly zeros, and the latency of their products is what
+// takes the time.  Here the nibbles stay integers: 8 inputs' nibbles become two words of signed bytes 16 * (nibble - 8) in
+// three instructions, and dp4a adds their products with the activations.  Those are integers
 // too, of 16 bits (bf16 and e4m3 activations) or 24 (fp32), as P signed bytes, with one fp32 scale per 16 inputs: an
 // activation is off by at most 2^-16 (2^-24) of the largest of its 16, far below what the output's type can show.
 // Sums of 16 products are exact in 32 bits.
