@@ -549,22 +549,52 @@ __host__ __device__ __forceinline__ int most_units(int rows, int E, int pass) { 
   return (rows < E ? rows : E) + rows / pass;
 }
 
-// One block makes the plan.  The place of a row in its expert's part of the list is whichever its atomic gives it: a row is a
-// column of its own in every product, and no result depends on which.
+// One block makes the plan.  An expert's rows stay in their order: the place of a row decides whether it comes into a unit of
+// one or of two tiles of rows, which add a group in different orders (many_step), so that it has to follow from topk_idx alone.
+// Each warp counts, and then places, a stretch of the rows; it places 32 at a time by the lanes that name the same expert.
 __device__ __forceinline__ void make_plan(const int* __restrict__ topk_idx, int rows, int E, int pass, ManyPlan* plan) {
-  __shared__ int count[1024], start[1024];
+  constexpr int ONCE = 4;  // turns of 32 rows whose loads are under way together
+  __shared__ int start[1024];  // rows of an expert, then the place of its first
+  // a warp's rows of an expert, then its next one's place among the expert's: 16 bits each, two to a word
+  __shared__ uint32_t own_words[kWarps][512];
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-  for (int e = threadIdx.x; e < E; e += 256) count[e] = 0;
+  unsigned short* own = reinterpret_cast<unsigned short*>(own_words[warp]);
+  const int stretch = (rows + kWarps * kWarp - 1) / (kWarps * kWarp) * kWarp, first = warp * stretch, last = min(first + stretch, rows);
+  auto each_turn = [&](auto use) {  // use(row, its expert; below zero: none, those are flagged by the combine)
+    for (int r0 = first; r0 < last; r0 += ONCE * kWarp) {
+      int id[ONCE];
+#pragma unroll
+      for (int i = 0; i < ONCE; ++i) {
+        const int r = r0 + i * kWarp + lane;
+        id[i] = r < last ? __ldg(topk_idx + r) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < ONCE; ++i)
+        if (r0 + i * kWarp < last) use(r0 + i * kWarp + lane, (unsigned)id[i] < (unsigned)E ? id[i] : -1);
+    }
+  };
+  for (int i = lane; i < (E + 1) / 2; i += kWarp) own_words[warp][i] = 0;
+  __syncwarp();
+  each_turn([&](int, int e) {
+    if (e >= 0) atomicAdd(&own_words[warp][e / 2], 1u << (16 * (e & 1)));
+  });
   __syncthreads();
-  for (int r = threadIdx.x; r < rows; r += 256) {
-    const int e = __ldg(topk_idx + r);
-    if ((unsigned)e < (unsigned)E) atomicAdd(&count[e], 1);  // others are flagged by the combine
+  for (int e = threadIdx.x; e < E; e += kWarps * kWarp) {
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      unsigned short* of = reinterpret_cast<unsigned short*>(own_words[w]) + e;
+      const int c = *of;
+      *of = (unsigned short)before;
+      before += c;
+    }
+    start[e] = before;
   }
   __syncthreads();
   if (warp == 0) {  // rows and units before each expert
     int before = 0, units = 0;
     for (int e0 = 0; e0 < E; e0 += kWarp) {
-      const int e = e0 + lane, c = e < E ? count[e] : 0, u = (c + pass - 1) / pass;
+      const int e = e0 + lane, c = e < E ? start[e] : 0, u = (c + pass - 1) / pass;
       int cs = c, us = u;
 #pragma unroll
       for (int o = 1; o < kWarp; o <<= 1) {
@@ -587,10 +617,14 @@ __device__ __forceinline__ void make_plan(const int* __restrict__ topk_idx, int 
   }
   __syncthreads();
   int* list = plan->unit + 3 * most_units(rows, E, pass);
-  for (int r = threadIdx.x; r < rows; r += 256) {
-    const int e = __ldg(topk_idx + r);
-    if ((unsigned)e < (unsigned)E) list[atomicAdd(&start[e], 1)] = r;
-  }
+  each_turn([&](int r, int e) {
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int before = __popc(same & ((1u << lane) - 1u)), at = e >= 0 ? own[e] : 0;
+    __syncwarp();
+    if (e >= 0 && before == 0) own[e] = (unsigned short)(at + __popc(same));
+    __syncwarp();
+    if (e >= 0) list[start[e] + at + before] = r;
+  });
 }
 
 // P planes of eight inputs each, in a word's order (0,4) (1,5) (2,6) (3,7).
