@@ -442,9 +442,9 @@ int moe_quantize_w4(const void* W, int E, int K, int N, int dtype, int group, vo
  * [T,k] fp32 (these three at any address of their type: rows of a larger batch may be passed as they are).
  * W1q, W3q: [E,f,h/2], W1s, W3s: [E,f,ceil(h/group)]; W2q: [E,h,f/2], W2s: [E,h,ceil(f/group)].  y: [T,h] dtype.
  * Sums are fp32 over the exact 4-bit values, a group's sum is scaled once.  One token (k <= 64), and up to 8 tokens with
- * T*k <= 12, that fit in shared memory: x and a are rounded to 16 (MOE_BF16) or 24 bits of the largest of 16 neighbours, and y sums the experts in ascending order instead of j's, whatever else is in the batch.
- * Otherwise x is read as it is (its values below 2^-34 of the largest of 128 neighbours apart), a keeps 11 or 23
- * significant bits, and the order of the fp32 sums may go by the batch's routing (deterministically).  An id outside
+ * T*k <= 12, that fit in shared memory: x and a are rounded to 24 bits of the largest of 16 neighbours (to zeros where that is below 2^-90), and y sums the experts in ascending order instead of j's, whatever else is in the batch.
+ * Otherwise x is read as it is (MOE_BF16, MOE_E4M3) or keeps 23 significant bits (MOE_F32), a keeps 11 (MOE_BF16) or 23, of both
+ * what is below 2^-34 of the largest of 128 neighbours is lost (all where that is below 2^-90; nothing of e4m3), and the order of the fp32 sums may go by the batch's routing (deterministically).  An id outside
  * [0,E) sets MOE_STATUS_BAD_INDEX and adds nothing.  A token with a value that is not a finite number gets NaN or
  * infinities, and no other token does.
  * Requires h % 32 == 0, f % 32 == 0, h*f < 2^32, 1 <= k <= E <= 1024 and T*k <= 65536.

@@ -9,7 +9,7 @@
 //
 // "Few" (one token, or up to 8 and 12 rows, whose activations fit in shared memory): integers through dp4a, see below.
 // Two launches: the first writes `a`, the second adds each token's outputs over its experts in registers; it starts early and has its
-// first weights under way while the first still runs.  Large layer, one token in 8 bits: 46 us (58% of the floor's rate;
+// first weights under way while the first still runs.  Large layer, one token in 8 bits: 52 us (51% of the floor's rate;
 // tensor cores in this place 86 us).  Small layer (h 2048, f 1408, 6 of 64): 14 us, of which the launches, the chain from
 // topk_idx to y and the host are most.
 //
@@ -54,10 +54,14 @@ constexpr int kStages = 2;       // turns of activations in shared memory (three
 // Rows of a unit of the many form.  With two planes a second tile of rows would take the registers that hide the latency
 // (13 tokens of the long-sequence layer: 92 us).
 template <int P> constexpr int kPass = P == 1 ? 16 : 8;
-constexpr int kFewBytes = 100 * 1024;  // shared memory for the few form's activations
-constexpr int kFewSteps = 128;         // of a warp: kFewBytes / (128 inputs x 2.25 bytes) / 8, and one more an expert
-// One token: blocks an SM, and steps of weights under way in a warp.  Large / Small layer, both kernels: 4, 1 and 4 46 / 14 us;
-// 3, 1 and 2 57 / 18; 2, 2 and 4 59 / 14.
+// Shared memory for the few form's activations.  One token may leave room for a single block of the second kernel on an SM (h
+// 4096, 8 experts, f 5632: 85 us, the many form 119; f 7168: 103 and 142); several are left to the many form then (4 tokens of
+// 3, h f 4096: 104 us, a block an SM 136).
+template <int ROWS> constexpr int kFewBytes = (ROWS == 1 ? 200 : 100) * 1024;
+constexpr int kFewSteps = 128;  // of a warp: kFewBytes / (128 inputs x 3.25 bytes) / 8, and one more an expert
+static_assert(kFewBytes<1> / (kStep / 16 * 52) / kWarps + kFewRows <= kFewSteps, "a warp's list holds its steps");
+// One token: blocks an SM of the first kernel, and steps of weights under way in a warp of either.  Large / Small layer, both
+// kernels: 4, 1 and 4 52 / 16.3 us; 3, 1 and 4 60 / 16.6; 3, 2 and 4 63 / 16.7; 2, 2 and 4 58 / 16.6; 4, 1 and 2 52.5 / 17.7.
 constexpr int kUpBlocks = 4, kUpAhead = 1, kDownAhead = 4;
 
 struct W4Mat {
@@ -106,9 +110,10 @@ __device__ __forceinline__ void place_of(int c, int* word, int* quarter) {
 // With one or two rows an expert the tensor cores would be fed mostly zeros, and the latency of their products is what
 // takes the time.  Here the nibbles stay integers: 8 inputs' nibbles become two words of signed bytes 16 * (nibble - 8) in
 // three instructions, and dp4a adds their products with the activations.  Those are integers
-// too, of 16 bits (bf16 and e4m3 activations) or 24 (fp32), as P signed bytes, with one fp32 scale per 16 inputs: an
-// activation is off by at most 2^-16 (2^-24) of the largest of its 16, far below what the output's type can show.
-// Sums of 16 products are exact in 32 bits.
+// too, of 24 bits as three signed bytes, with one fp32 scale per 16 inputs: an activation is off by at most 2^-24 of the
+// largest of its 16, as much as an fp32 sum of the 16 may lose.  (Two bytes, 16 bits, took 47 us where three take 52, but
+// an input 2000 times its neighbours left these four bits of their own: where its weights are small or zero, outputs were off by
+// more than their type's rounding.)  Sums of 16 products are exact in 32 bits.
 //
 // Also measured for a token of the Large layer: bulk copies of the rows into shared memory (pieces of 512 bytes: 76 us, of
 // 1024: 70, the copies are too small), and a warp along 1024 inputs of one output instead of 16 outputs x 128 (57 to 75).
@@ -120,7 +125,7 @@ struct FewArgs {
   const float* topk_w;
   int T, k, E, K, N;      // K inputs, N outputs
   W4Mat mat[2];
-  unsigned char* bytes;   // `a` as integers: [T*k][f/16][P][16]
+  unsigned char* bytes;   // `a` as integers: [T*k][f/16][3][16]
   float* scales;          // and its scales: [T*k][f/16]
   void* y;                // down: y [T, N]
   int* status;
@@ -137,30 +142,25 @@ __device__ __forceinline__ unsigned long long bits_of(unsigned long long mask, i
   return (mask >> (t * k)) & (k < 64 ? (1ull << k) - 1ull : ~0ull);
 }
 
-// The largest integer used, somewhat below P signed bytes 127, 127, ... (8355711 for three: a product with fp32's 24 bits may
-// end a unit above).
-template <int P> constexpr float kMostInt = P == 2 ? 32630.f : 8355000.f;
+// The largest integer used, somewhat below three signed bytes 127, 127, 127 (a product with fp32's 24 bits may end a unit above).
+constexpr int kPlanes = 3;
+constexpr float kMostInt = 8355000.f;
 
 // Scale of 16 values whose largest magnitude has the pattern `amax`, and its inverse.  Values that are no finite numbers
 // make it NaN; below 2^-90 all count as zeros.  The scale carries the 1/16 of the weights' bytes.
-template <int P>
 __device__ __forceinline__ float int_scale(uint32_t amax, float* inverse) {
   const float m = __uint_as_float(amax);
-  *inverse = m < 0x1p-90f || amax >= 0x7f800000u ? 0.f : kMostInt<P> / m;
-  return amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : m < 0x1p-90f ? 0.f : m * (1.0f / (16.0f * kMostInt<P>));
+  *inverse = m < 0x1p-90f || amax >= 0x7f800000u ? 0.f : kMostInt / m;
+  return amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : m < 0x1p-90f ? 0.f : m * (1.0f / (16.0f * kMostInt));
 }
 // Byte planes of four integers, the highest first: a lower plane's bytes are the integers' own (read as signed they are up
 // to 128 too small, which is added before the next shift).
-template <int P>
 __device__ __forceinline__ void int_planes(int q0, int q1, int q2, int q3, uint32_t* plane) {
   auto bytes = [](int x0, int x1, int x2, int x3, uint32_t from) {  // byte 0 or 1 of each
     return __byte_perm(__byte_perm(x0, x1, from), __byte_perm(x2, x3, from), 0x5410);
   };
-#pragma unroll
-  for (int p = P - 1; p > 1; --p) {
-    plane[p] = bytes(q0, q1, q2, q3, 0x0040);
-    q0 = (q0 + 128) >> 8; q1 = (q1 + 128) >> 8; q2 = (q2 + 128) >> 8; q3 = (q3 + 128) >> 8;
-  }
+  plane[2] = bytes(q0, q1, q2, q3, 0x0040);
+  q0 = (q0 + 128) >> 8; q1 = (q1 + 128) >> 8; q2 = (q2 + 128) >> 8; q3 = (q3 + 128) >> 8;
   plane[1] = bytes(q0, q1, q2, q3, 0x0040);
   plane[0] = bytes(q0 + 128, q1 + 128, q2 + 128, q3 + 128, 0x0051);
 }
@@ -189,57 +189,52 @@ __device__ __forceinline__ void load16(const E4M3* p, float* f) {
   }
 }
 
-// A lane's activations of a step: its four words' inputs, P bytes each, and their scales (one for two words, with
-// groups of 32 one a word).  Rows in shared memory are padded to whole steps with zeros.
-template <int P, int G>
-struct IntActs {
-  static constexpr int kScales = G == 32 ? 4 : 2;
-  uint32_t q[P][4][2];
-  float s[kScales];
-
-  // bytes, scale: the row's at the lane's first input k of the step (k / 16 pieces from the row's start)
-  __device__ __forceinline__ void load(const unsigned char* bytes, const float* scale, int k) {
+// Of a lane's inputs of a step, the sums for N outputs: w their words, g their groups' scales.  A lane has one scale for two
+// words, with groups of 32 one a word.  bytes, scale: the row's in shared memory at the lane's first input k of the step (k / 16
+// pieces from the row's start); rows are padded to whole steps with zeros.
+template <int G, int N>
+__device__ __forceinline__ void int_dots(const unsigned char* bytes, const float* scale, int k, const uint32_t* const* w,
+                                         const __nv_bfloat16* const* g, float* sum) {
+  constexpr int SCALES = G == 32 ? 4 : 2, WORDS = 4 / SCALES;
 #pragma unroll
-    for (int i = 0; i < kScales; ++i) {
-      const int block = G == 128 ? i : i * (G / 16);  // of one or two words
-      s[i] = scale[block];
+  for (int i = 0; i < SCALES; ++i) {
+    const int block = G == 128 ? i : i * (G / 16);  // of one or two words
+    uint32_t q[kPlanes][WORDS][2];
+    const float s = scale[block];
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const unsigned char* b = bytes + (block * P + p) * 16;
-        if constexpr (G == 32) {
-          const uint2 u = *reinterpret_cast<const uint2*>(b + (k & 8));
-          q[p][i][0] = u.x; q[p][i][1] = u.y;
-        } else {
-          const uint4 u = *reinterpret_cast<const uint4*>(b);
-          q[p][2 * i][0] = u.x; q[p][2 * i][1] = u.y; q[p][2 * i + 1][0] = u.z; q[p][2 * i + 1][1] = u.w;
-        }
+    for (int p = 0; p < kPlanes; ++p) {
+      const unsigned char* b = bytes + (block * kPlanes + p) * 16;
+      if constexpr (G == 32) {
+        const uint2 u = *reinterpret_cast<const uint2*>(b + (k & 8));
+        q[p][0][0] = u.x; q[p][0][1] = u.y;
+      } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(b);
+        q[p][0][0] = u.x; q[p][0][1] = u.y; q[p][WORDS - 1][0] = u.z; q[p][WORDS - 1][1] = u.w;
       }
     }
-  }
-  // Sum over the lane's inputs of the step of one output: w its words, g the groups' scales.
-  __device__ __forceinline__ float dot(const uint32_t* w, const __nv_bfloat16* g) const {
-    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kScales; ++i) {
-      constexpr int WORDS = 4 / kScales;
-      int d[P];
+    for (int n = 0; n < N; ++n) {
+      int d[kPlanes];
 #pragma unroll
-      for (int p = 0; p < P; ++p) d[p] = 0;
+      for (int p = 0; p < kPlanes; ++p) d[p] = 0;
 #pragma unroll
       for (int j = 0; j < WORDS; ++j) {
         // the signed bytes 16 (nibble - 8): even inputs, odd inputs
-        const int even = (int)(((w[i * WORDS + j] << 4) ^ 0x88888888u) & 0xf0f0f0f0u);
-        const int odd = (int)((w[i * WORDS + j] ^ 0x88888888u) & 0xf0f0f0f0u);
+        const uint32_t word = w[n][i * WORDS + j];
+        const int even = (int)(((word << 4) ^ 0x88888888u) & 0xf0f0f0f0u), odd = (int)((word ^ 0x88888888u) & 0xf0f0f0f0u);
 #pragma unroll
-        for (int p = 0; p < P; ++p) d[p] = __dp4a(odd, (int)q[p][i * WORDS + j][1], __dp4a(even, (int)q[p][i * WORDS + j][0], d[p]));
+        for (int p = 0; p < kPlanes; ++p) d[p] = __dp4a(odd, (int)q[p][j][1], __dp4a(even, (int)q[p][j][0], d[p]));
       }
-      const float v = P == 2 ? (float)(d[0] * 256 + d[1]) : fmaf((float)(d[0] * 256 + d[1]), 256.f, (float)d[P - 1]);
-      if constexpr (G == 128) sum = i == 0 ? v * s[i] : fmaf(v, s[i], sum);
-      else sum = fmaf(v * s[i], __bfloat162float(g[i]), sum);
+      const float v = fmaf((float)(d[0] * 256 + d[1]), 256.f, (float)d[2]);
+      if constexpr (G == 128) sum[n] = i == 0 ? v * s : fmaf(v, s, sum[n]);
+      else sum[n] = fmaf(v * s, __bfloat162float(g[n][i]), i == 0 ? 0.f : sum[n]);
     }
-    return G == 128 ? sum * __bfloat162float(g[0]) : sum;
   }
-};
+  if constexpr (G == 128) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) sum[n] *= __bfloat162float(g[n][0]);
+  }
+}
 
 // A lane's words and scales of a step, for outputs g and g + 8 of MATS matrices.
 template <int G, int MATS>
@@ -278,10 +273,10 @@ struct IntWeights {
 
 // `a` of 32 outputs of the slot's expert for the tokens that chose it: two tiles of outputs, the inputs' steps over four
 // warps each.  One slot a row of topk_idx: the first row of an expert does them all.  ROWS: 1 for one token, else 8.
-template <typename X, int P, int G, int ROWS>
+template <typename X, int G, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few_up_kernel(const __grid_constant__ FewArgs a) {
   constexpr int AHEAD = kUpAhead, SPLIT = kWarps / 2;
-  extern __shared__ uint4 acts[];  // bytes [row][8 S][P][16], then scales [row][8 S]
+  extern __shared__ uint4 acts[];  // bytes [row][8 S][3][16], then scales [row][8 S]
   __shared__ float red[kWarps][2][kTile][ROWS + (ROWS > 1)];
   __shared__ int token[kFewTokens];
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, tile = warp / SPLIT, part = warp % SPLIT;
@@ -317,7 +312,7 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few
   const int n = __popc(chosen);
   if (mine) token[__popc(chosen & ((1u << lane) - 1u))] = lane;  // every warp writes the same
   __syncwarp();
-  float* scales = reinterpret_cast<float*>(acts + (size_t)n * blocks * P);
+  float* scales = reinterpret_cast<float*>(acts + (size_t)n * blocks * kPlanes);
   for (int r = 0; r < n; ++r) {
     const X* x = static_cast<const X*>(a.x) + (size_t)token[r] * a.K;
     for (int i = threadIdx.x; i < blocks; i += kWarps * 32) {
@@ -326,22 +321,22 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few
       uint32_t amax = 0;
 #pragma unroll
       for (int c = 0; c < 16; ++c) amax = max(amax, __float_as_uint(f[c]) & 0x7fffffffu);
-      float scale = int_scale<P>(amax, &inverse);
+      float scale = int_scale(amax, &inverse);
       if constexpr (sizeof(X) == 1) scale *= __ldg(a.x_scale + (size_t)token[r] * S + i / 8);
       scales[r * blocks + i] = scale;
-      uint32_t word[4][P];
+      uint32_t word[4][kPlanes];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {  // of eight inputs the even ones, then the odd ones
         const float* v = f + c / 2 * 8 + (c & 1);
-        int_planes<P>(__float2int_rn(v[0] * inverse), __float2int_rn(v[2] * inverse), __float2int_rn(v[4] * inverse),
-                      __float2int_rn(v[6] * inverse), word[c]);
+        int_planes(__float2int_rn(v[0] * inverse), __float2int_rn(v[2] * inverse), __float2int_rn(v[4] * inverse),
+                   __float2int_rn(v[6] * inverse), word[c]);
       }
 #pragma unroll
-      for (int p = 0; p < P; ++p) acts[(r * blocks + i) * P + p] = make_uint4(word[0][p], word[1][p], word[2][p], word[3][p]);
+      for (int p = 0; p < kPlanes; ++p) acts[(r * blocks + i) * kPlanes + p] = make_uint4(word[0][p], word[1][p], word[2][p], word[3][p]);
     }
   }
   __syncthreads();
-  const unsigned char* bytes = reinterpret_cast<const unsigned char*>(acts) + (part * 8 + at.k / 16) * (16 * P);
+  const unsigned char* bytes = reinterpret_cast<const unsigned char*>(acts) + (part * 8 + at.k / 16) * (16 * kPlanes);
   const float* scale = scales + part * 8 + at.k / 16;
   float acc[2][2][ROWS] = {};
   for (int s0 = part; s0 < S; s0 += SPLIT * AHEAD) {
@@ -351,14 +346,16 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
         if (r >= n) break;
-        IntActs<P, G> x;
-        x.load(bytes + r * blocks * (16 * P), scale + r * blocks, at.k);
+        const uint32_t* words[4] = {w[d].w[0][0], w[d].w[0][1], w[d].w[1][0], w[d].w[1][1]};
+        const __nv_bfloat16* groups[4] = {w[d].s[0][0], w[d].s[0][1], w[d].s[1][0], w[d].s[1][1]};
+        float sum[4];
+        int_dots<G, 4>(bytes + r * blocks * (16 * kPlanes), scale + r * blocks, at.k, words, groups, sum);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int o = 0; o < 2; ++o) acc[m][o][r] += x.dot(w[d].w[m][o], w[d].s[m][o]);
+          for (int o = 0; o < 2; ++o) acc[m][o][r] += sum[m * 2 + o];
       }
-      bytes += SPLIT * 8 * (16 * P);
+      bytes += SPLIT * 8 * (16 * kPlanes);
       scale += SPLIT * 8;
       load(w[d]);
     }
@@ -388,13 +385,13 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few
 #pragma unroll
     for (int c = 8; c > 0; c >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, c));
     float inverse;
-    const float sx = int_scale<P>(amax, &inverse);
+    const float sx = int_scale(amax, &inverse);
     if (on) {
       const size_t row = (size_t)token[r] * a.k + __ffsll(bits_of(mask, token[r], a.k)) - 1, block = row * (a.N / 16) + blockIdx.x * 2 + t;
-      uint32_t plane[P];
-      int_planes<P>(__float2int_rn(value * inverse), 0, 0, 0, plane);
+      uint32_t plane[kPlanes];
+      int_planes(__float2int_rn(value * inverse), 0, 0, 0, plane);
 #pragma unroll
-      for (int p = 0; p < P; ++p) a.bytes[(block * P + p) * 16 + byte_place(o)] = (unsigned char)plane[p];
+      for (int p = 0; p < kPlanes; ++p) a.bytes[(block * kPlanes + p) * 16 + byte_place(o)] = (unsigned char)plane[p];
       if (o == 0) a.scales[block] = sx;
     }
   }
@@ -402,10 +399,10 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 1 ? kUpBlocks : 2) w4_few
 
 // y of 16 outputs for all tokens: the steps of all experts' products over the warps, each token's sum over its experts in
 // registers.
-template <typename T, int P, int G, int ROWS, int BLOCKS>
+template <typename T, int G, int ROWS, int BLOCKS>
 __global__ void __launch_bounds__(kWarps * 32, BLOCKS) w4_few_down_kernel(const __grid_constant__ FewArgs a) {
   constexpr int AHEAD = kDownAhead;
-  extern __shared__ uint4 acts[];  // `a`: bytes [row][8 S][P][16], then scales [row][8 S]
+  extern __shared__ uint4 acts[];  // `a`: bytes [row][8 S][3][16], then scales [row][8 S]
   __shared__ float red[kWarps][kTile][ROWS + (ROWS > 1)];
   __shared__ int expert[kFewRows], row[kFewRows][ROWS], idx[kFewRows];
   __shared__ float weight[kFewRows][ROWS];
@@ -474,21 +471,22 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS) w4_few_down_kernel(const 
   };
 #pragma unroll
   for (int d = 0; d < AHEAD; ++d) load(w[d]);
-  float* scales = reinterpret_cast<float*>(acts + (size_t)rows * blocks * P);
+  float* scales = reinterpret_cast<float*>(acts + (size_t)rows * blocks * kPlanes);
   if (a.K % kStep != 0) {  // the padding of a row's last step
     const int inside = a.K / 16, pad = blocks - inside;
     for (int i = threadIdx.x; i < rows * pad; i += kWarps * 32) {
       const int to = i / pad * blocks + inside + i % pad;
       scales[to] = 0.f;
 #pragma unroll
-      for (int p = 0; p < P; ++p) acts[to * P + p] = make_uint4(0, 0, 0, 0);
+      for (int p = 0; p < kPlanes; ++p) acts[to * kPlanes + p] = make_uint4(0, 0, 0, 0);
     }
   }
   wait_dependency();  // `a` is read from here on; the weights above are nobody's output
   // copies alone, so that no thread waits for one before it starts the next
   for (int r = 0; r < rows; ++r) {
-    const uint4* from = reinterpret_cast<const uint4*>(a.bytes) + (size_t)r * (a.K / 16) * P;
-    for (int i = threadIdx.x; i < a.K / 16 * P; i += kWarps * 32) ptx::cp_async_16(ptx::smem_u32(acts + r * blocks * P + i), from + i, 16);
+    const uint4* from = reinterpret_cast<const uint4*>(a.bytes) + (size_t)r * (a.K / 16) * kPlanes;
+    for (int i = threadIdx.x; i < a.K / 16 * kPlanes; i += kWarps * 32)
+      ptx::cp_async_16(ptx::smem_u32(acts + r * blocks * kPlanes + i), from + i, 16);
     const float* from_scale = a.scales + (size_t)r * (a.K / 16);
     for (int i = threadIdx.x; i < a.K / 16; i += kWarps * 32) ptx::cp_async_4(ptx::smem_u32(scales + r * blocks + i), from_scale + i);
   }
@@ -505,10 +503,13 @@ __global__ void __launch_bounds__(kWarps * 32, BLOCKS) w4_few_down_kernel(const 
       for (int t = 0; t < ROWS; ++t) {
         const int r = row[l][t];
         if (ROWS > 1 && r < 0) continue;
-        IntActs<P, G> x;
-        x.load(reinterpret_cast<const unsigned char*>(acts) + (r * blocks + block) * (16 * P), scales + r * blocks + block, at.k);
+        const uint32_t* words[2] = {w[d].w[0][0], w[d].w[0][1]};
+        const __nv_bfloat16* groups[2] = {w[d].s[0][0], w[d].s[0][1]};
+        float sum[2];
+        int_dots<G, 2>(reinterpret_cast<const unsigned char*>(acts) + (r * blocks + block) * (16 * kPlanes), scales + r * blocks + block,
+                       at.k, words, groups, sum);
 #pragma unroll
-        for (int o = 0; o < 2; ++o) acc[o][t] = fmaf(x.dot(w[d].w[0][o], w[d].s[0][o]), weight[l][t], acc[o][t]);
+        for (int o = 0; o < 2; ++o) acc[o][t] = fmaf(sum[o], weight[l][t], acc[o][t]);
       }
       load(w[d]);
     }
@@ -1039,12 +1040,9 @@ void launch_early(void (*kernel)(A), dim3 grid, int threads, size_t bytes, cudaS
   count_launch(st);
 }
 
-template <typename T> constexpr int kIntPlanes = sizeof(T) == 2 ? 2 : 3;  // bytes of an activation, few form
-
 // Shared memory of `rows` rows of K activations in the few form.
-template <typename T>
 size_t few_bytes(int rows, int K) {
-  return (size_t)rows * ((K + kStep - 1) / kStep) * 8 * (16 * kIntPlanes<T> + sizeof(float));
+  return (size_t)rows * ((K + kStep - 1) / kStep) * 8 * (16 * kPlanes + sizeof(float));
 }
 
 template <typename K>
@@ -1059,28 +1057,27 @@ void allow_shared(K kernel, int bytes, bool* ready) {  // per device: the attrib
 
 template <typename X, typename T, int G, int ROWS>
 void few(const W4Ffn& p, cudaStream_t st) {
-  constexpr int P = kIntPlanes<T>;
   unsigned char* bytes = static_cast<unsigned char*>(p.a);
-  float* scales = reinterpret_cast<float*>(bytes + (size_t)p.T * p.k * p.f * P);
+  float* scales = reinterpret_cast<float*>(bytes + (size_t)p.T * p.k * p.f * kPlanes);
   const FewArgs up{p.x, p.x_scale, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.h, p.f,
                    {{static_cast<const unsigned char*>(p.W1q), static_cast<const __nv_bfloat16*>(p.W1s)},
                     {static_cast<const unsigned char*>(p.W3q), static_cast<const __nv_bfloat16*>(p.W3s)}}, bytes, scales, nullptr, p.status};
   static bool ready[3][64] = {};
-  allow_shared(w4_few_up_kernel<X, P, G, ROWS>, kFewBytes, ready[0]);
-  w4_few_up_kernel<X, P, G, ROWS><<<dim3(p.f / (2 * kTile), p.T * p.k), kWarps * 32, few_bytes<T>(p.T, p.h), st>>>(up);
+  allow_shared(w4_few_up_kernel<X, G, ROWS>, kFewBytes<ROWS>, ready[0]);
+  w4_few_up_kernel<X, G, ROWS><<<dim3(p.f / (2 * kTile), p.T * p.k), kWarps * 32, few_bytes(p.T, p.h), st>>>(up);
   count_launch(st);
   const FewArgs down{nullptr, nullptr, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.f, p.h,
                      {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, bytes, scales, p.y, p.status};
   // One token's second kernel with three blocks an SM spills some of its registers, which a grid of more than two an SM is
   // glad to pay (Large layer: 46 us for both kernels, 51 with two) and a smaller one is not (Small layer: 17 and 14 us).
-  const size_t shared = few_bytes<T>(p.T * p.k, p.f);
+  const size_t shared = few_bytes(p.T * p.k, p.f);
   const int blocks = p.h / kTile;
   if (ROWS == 1 && blocks > 2 * num_sms()) {
-    allow_shared(w4_few_down_kernel<T, P, G, ROWS, ROWS == 1 ? 3 : 2>, kFewBytes, ready[2]);
-    launch_early(w4_few_down_kernel<T, P, G, ROWS, ROWS == 1 ? 3 : 2>, dim3(blocks), kWarps * 32, shared, st, down);
+    allow_shared(w4_few_down_kernel<T, G, ROWS, ROWS == 1 ? 3 : 2>, kFewBytes<ROWS>, ready[2]);
+    launch_early(w4_few_down_kernel<T, G, ROWS, ROWS == 1 ? 3 : 2>, dim3(blocks), kWarps * 32, shared, st, down);
   } else {
-    allow_shared(w4_few_down_kernel<T, P, G, ROWS, 2>, kFewBytes, ready[1]);
-    launch_early(w4_few_down_kernel<T, P, G, ROWS, 2>, dim3(blocks), kWarps * 32, shared, st, down);
+    allow_shared(w4_few_down_kernel<T, G, ROWS, 2>, kFewBytes<ROWS>, ready[1]);
+    launch_early(w4_few_down_kernel<T, G, ROWS, 2>, dim3(blocks), kWarps * 32, shared, st, down);
   }
 }
 
@@ -1153,10 +1150,11 @@ void many(const W4Ffn& p, cudaStream_t st) {
 template <typename X, typename T, int G>
 void run_group(const W4Ffn& p, cudaStream_t st) {
   // Several tokens: the few form's second kernel does its rows one after another (8 rows of 2 tokens, h 1024, f 512: 12 us and
-  // in the many form 17; 12 rows of the Small layer: 35 and 33; 18 rows, h 832, f 1408: 46 and 36; 24 of the Small layer 59
-  // and 52).
-  const bool is_few = p.T <= kFewTokens && p.T * p.k <= (p.T == 1 ? kFewRows : kSeveralRows) && few_bytes<T>(p.T, p.h) <= (size_t)kFewBytes &&
-                      few_bytes<T>(p.T * p.k, p.f) <= (size_t)kFewBytes;
+  // in the many form 17; 10 rows of the Small layer 33 and 35, 12 38 and 37; in fp32 12 rows 38 and 39; 18 rows, h 832, f 1408, 46
+  // and 36).
+  const size_t most = p.T == 1 ? kFewBytes<1> : kFewBytes<kFewTokens>;
+  const bool is_few = p.T <= kFewTokens && p.T * p.k <= (p.T == 1 ? kFewRows : kSeveralRows) && few_bytes(p.T, p.h) <= most &&
+                      few_bytes(p.T * p.k, p.f) <= most;
   if (!is_few) many<X, T, G>(p, st);
   else if (p.T == 1) few<X, T, G, 1>(p, st);
   else few<X, T, G, kFewTokens>(p, st);
