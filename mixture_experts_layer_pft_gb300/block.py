@@ -93,10 +93,11 @@ class DecodeBlock:
         W1 = params["W1"]
         E, h, f = W1.shape
         dt, dev = W1.dtype, W1.device
-        self.params, self.E, self.h, self.f, self.k, self.group, self.eps = params, E, h, f, k, group, eps
+        self.params, self.T, self.E, self.h, self.f, self.k, self.group, self.eps = params, T, E, h, f, k, group, eps
         self.gate, self.renorm, self.dtype = gate, renorm, dt
-        self.ws = torch.zeros(max(B.workspace_size(op, T, h, E, k, f, dt) for op in (B.MOE_OP_ROUTE, B.MOE_OP_EXPERT_FFN_W4)),
-                              dtype=torch.uint8, device=dev)
+        # a router over fewer tokens may split its sums further and need more
+        route = max(B.workspace_size(B.MOE_OP_ROUTE, n, h, E, k, f, dt) for n in range(T + 1))
+        self.ws = torch.zeros(max(route, B.workspace_size(B.MOE_OP_EXPERT_FFN_W4, T, h, E, k, f, dt)), dtype=torch.uint8, device=dev)
         self.w4 = []
         for name in ("W1", "W3", "W2"):
             _, K, N = params[name].shape
@@ -113,11 +114,15 @@ class DecodeBlock:
         self.topk_idx, self.topk_w = torch.empty(T, k, dtype=torch.int32, **d), torch.empty(T, k, **d)
 
     def step(self, x: torch.Tensor, residual: torch.Tensor):
-        """(y, s) of a batch of the block's T tokens."""
-        p = self.params
-        B.moe_add_rmsnorm(x, residual, p["gamma"], self.eps, self.s, self.n, self.q, self.q_scale, None, self.ws)
-        B.moe_route(self.n, p["Wg"], p.get("bias"), self.k, self.logits, self.probs, self.topk_idx, self.topk_w, self.ws,
-                    gate=self.gate, renorm=self.renorm)
-        B.moe_expert_ffn_w4(self.q if self.act8 else self.n, self.q_scale, self.topk_idx, self.topk_w, *self.w4, self.group,
-                            self.y, self.ws)
-        return self.y, self.s
+        """(y, s) of a batch of at most the block's T tokens: rows of the block's own buffers, which the next step overwrites."""
+        p, n = self.params, x.shape[0]
+        if n > self.T:
+            raise ValueError(f"a batch of {n} tokens for a block of {self.T}")
+        own = (self.s, self.n, self.y, self.q, self.q_scale, self.logits, self.probs, self.topk_idx, self.topk_w)
+        if n != self.T:
+            own = [t if t is None else t[:n] for t in own]
+        s, normed, y, q, q_scale, logits, probs, topk_idx, topk_w = own
+        B.moe_add_rmsnorm(x, residual, p["gamma"], self.eps, s, normed, q, q_scale, None, self.ws)
+        B.moe_route(normed, p["Wg"], p.get("bias"), self.k, logits, probs, topk_idx, topk_w, self.ws, gate=self.gate, renorm=self.renorm)
+        B.moe_expert_ffn_w4(q if self.act8 else normed, q_scale, topk_idx, topk_w, *self.w4, self.group, y, self.ws)
+        return y, s
