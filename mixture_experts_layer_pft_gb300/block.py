@@ -86,14 +86,16 @@ class AdamW:
 class DecodeBlock:
     """A block whose experts are in 4 bits, for decode steps of up to ``T`` tokens.
 
-    ``act8`` (bf16 blocks): the experts read the norm's 8-bit output; the router always reads the full one."""
+    ``act8`` (bf16 blocks): the experts read the norm's 8-bit output; the router always reads the full one.  Of ``params`` the
+    block keeps gamma, Wg and the bias: W1, W3 and W2 may be freed once they are quantised."""
 
     def __init__(self, params: dict, T: int, k: int, group: int = 128, act8: bool = True, eps: float = 1e-6,
                  gate: str = "softmax", renorm: bool = False):
         W1 = params["W1"]
         E, h, f = W1.shape
         dt, dev = W1.dtype, W1.device
-        self.params, self.T, self.E, self.h, self.f, self.k, self.group, self.eps = params, T, E, h, f, k, group, eps
+        self.T, self.E, self.h, self.f, self.k, self.group, self.eps = T, E, h, f, k, group, eps
+        self.params = {name: params.get(name) for name in ("gamma", "Wg", "bias")}
         self.gate, self.renorm, self.dtype = gate, renorm, dt
         # a router over fewer tokens may split its sums further and need more
         route = max(B.workspace_size(B.MOE_OP_ROUTE, n, h, E, k, f, dt) for n in range(T + 1))
@@ -123,6 +125,6 @@ class DecodeBlock:
             own = [t if t is None else t[:n] for t in own]
         s, normed, y, q, q_scale, logits, probs, topk_idx, topk_w = own
         B.moe_add_rmsnorm(x, residual, p["gamma"], self.eps, s, normed, q, q_scale, None, self.ws)
-        B.moe_route(normed, p["Wg"], p.get("bias"), self.k, logits, probs, topk_idx, topk_w, self.ws, gate=self.gate, renorm=self.renorm)
+        B.moe_route(normed, p["Wg"], p["bias"], self.k, logits, probs, topk_idx, topk_w, self.ws, gate=self.gate, renorm=self.renorm)
         B.moe_expert_ffn_w4(q if self.act8 else normed, q_scale, topk_idx, topk_w, *self.w4, self.group, y, self.ws)
         return y, s

@@ -1,4 +1,4 @@
-"""DecodeBlock: batches of fewer tokens than it was made for."""
+"""DecodeBlock: batches of fewer tokens than it was made for, and what of the parameters it keeps."""
 
 import gc
 import weakref
@@ -51,3 +51,14 @@ def test_the_workspace_holds_any_smaller_batch(block):
     for n in (520, 512, 257, 256, 1):
         y, s = dec.step(x[:n], x[:n])
         assert y.shape == (n, h) and (y == 0).all()
+
+
+def test_full_weights_are_not_kept(block):
+    p = params(64, 32, 4, torch.bfloat16)
+    held = [weakref.ref(p[n]) for n in ("W1", "W3", "W2")]
+    dec = block.DecodeBlock(p, 1, 2, group=32)
+    p = {n: p[n] for n in ("gamma", "Wg", "bias")}
+    gc.collect()
+    assert all(r() is None for r in held)
+    x = torch.ones(1, 64, dtype=torch.bfloat16, device="cuda")
+    assert torch.isfinite(dec.step(x, x)[0].float()).all()
