@@ -373,6 +373,8 @@ int moe_gshard_combine(const float* combine_w, const void* ye, int T, int E, int
  *   v = s * rstd * gamma (fp32);  y = round(v);
  *   q = e4m3(v / q_scale), round to nearest even, values beyond +-448 * q_scale saturate;
  *   q_scale[t,g] = max(amax of v over columns 128 g .. 128 g + 127, 2^-100) / 448.
+ * Where amax is above 2^-100, the quotient v / q_scale is taken as s*gamma * (448 / amax of |s*gamma|), in which rstd
+ * cancels: a value within fp32's rounding of the middle between two codes may get either.
  * The norm is of the stored (rounded) s, which is what the backward reads.  A NaN stays a NaN in s, y
  * and q, and leaves q_scale to the group's other columns.
  * x, residual, s, y: [T,h] dtype.  residual NULL: s is x itself, and the argument s must be NULL.

@@ -11,6 +11,7 @@
 // copies, see there; the same rows with ds_add: 235 MB in 42 us (82%), dgamma's second kernel included.  Sums run in fp32
 // in a fixed order: no atomics, bitwise reproducible.
 #include <cuda_fp8.h>
+#include <float.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -109,6 +110,10 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* 
   if (!on) return;
   if (rstd != nullptr && lt == 0) rstd[t] = rs;
   const int groups = (h + kQGroup - 1) / kQGroup;
+  // rstd in two factors, a power of two and one from [1, 2): s by the first is exact, and its product with gamma is at an end
+  // of fp32 only where the output is
+  const bool ordinary = rs > 0.f && rs <= FLT_MAX;
+  const float power = ordinary ? __uint_as_float(__float_as_uint(rs) & 0x7f800000u) : 1.0f, rest = rs / power;
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int v = lt + u * tpr;
@@ -117,14 +122,15 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* 
 #pragma unroll
       for (int i = 0; i < VN; i += 4) {
         const float4 g = load4(gamma + (size_t)v * VN + i);
-        f[u][i] *= g.x; f[u][i + 1] *= g.y; f[u][i + 2] *= g.z; f[u][i + 3] *= g.w;
+        f[u][i] = f[u][i] * power * g.x; f[u][i + 1] = f[u][i + 1] * power * g.y;
+        f[u][i + 2] = f[u][i + 2] * power * g.z; f[u][i + 3] = f[u][i + 3] * power * g.w;
       }
 #pragma unroll
       for (int i = 0; i < VN; ++i) amax = fmaxf(amax, fabsf(f[u][i]));
       if (y != nullptr) {
         float o[VN];
 #pragma unroll
-        for (int i = 0; i < VN; ++i) o[i] = f[u][i] * rs;
+        for (int i = 0; i < VN; ++i) o[i] = f[u][i] * rest;
         reinterpret_cast<uint4*>(y)[row + v] = pack(o, T());
       }
     }
@@ -132,9 +138,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* 
       // 128 columns are kQGroup / VN neighbouring lanes (tpr is a multiple of 32)
 #pragma unroll
       for (int o = kQGroup / VN / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      // rstd cancels in y / scale: without it a code has two roundings less that may push it over a tie
-      const float most = rs * amax, scale = fmaxf(most, 0x1p-100f) / 448.0f;
-      const float inv = most >= 0x1p-100f ? 448.0f / amax : rs * (448.0f * 0x1p100f);
+      // `rest` cancels in y / scale: without it a code has two roundings less that may push it over a tie
+      const float most = rest * amax, scale = fmaxf(most, 0x1p-100f) / 448.0f;
+      const float inv = most >= 0x1p-100f ? 448.0f / amax : rest * (448.0f * 0x1p100f);
       if (v < nvec) {
         if (v % (kQGroup / VN) == 0) q_scale[(size_t)t * groups + v / (kQGroup / VN)] = scale;
         store_q<VN>(q + (row + v) * VN, f[u], inv);
