@@ -375,8 +375,9 @@ int moe_gshard_combine(const float* combine_w, const void* ye, int T, int E, int
  *   q_scale[t,g] = max(amax of v over columns 128 g .. 128 g + 127, 2^-100) / 448.
  * Where amax is above 2^-100, the quotient v / q_scale is taken as s*gamma * (448 / amax of |s*gamma|), in which rstd
  * cancels: a value within fp32's rounding of the middle between two codes may get either.
- * The norm is of the stored (rounded) s, which is what the backward reads.  A NaN stays a NaN in s, y
- * and q, and leaves q_scale to the group's other columns.
+ * The norm is of the stored (rounded) s, which is what the backward reads.  A NaN in x or residual is in the row's rstd, so
+ * that all of the row's y and q are NaN, and its q_scale is 2^-100 / 448.  A NaN in gamma is in its column of y and q, and
+ * leaves q_scale to the group's other columns.
  * x, residual, s, y: [T,h] dtype.  residual NULL: s is x itself, and the argument s must be NULL.
  * gamma: [h] fp32.  y may be NULL when q is given; q ([T,h] bytes) and q_scale ([T,ceil(h/128)] fp32)
  * are both given or both NULL.  rstd: [T] fp32 or NULL.  s may be x or residual itself.
