@@ -79,7 +79,7 @@ _marshal = None  # the module that checks tensors and takes their addresses (csr
 
 def lib() -> ctypes.CDLL:
     """Load libmoe_pft.so once; raise if it is not built."""
-    global _lib, _marshal
+    global _lib
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is not built: run __graft_entry__.build() first")
@@ -88,11 +88,20 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
-        from . import _marshal as M
-
-        _marshal = M
         _lib = L
     return _lib
+
+
+def _checks():
+    """The checking module, loaded by the first call that needs it; raise if it is not built."""
+    global _marshal
+    if _marshal is None:
+        try:
+            from . import _marshal as M
+        except ImportError as e:
+            raise RuntimeError(f"_marshal.so is not built for this Python and torch ({e}): run __graft_entry__.build() first") from e
+        _marshal = M
+    return _marshal
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -327,9 +336,7 @@ def moe_gshard_combine(combine_w, ye, y, ws):
 
 def _check(t, name, dtype, shape):
     """Refuse a tensor whose type, shape or place the call would misread (None passes); returns its address."""
-    if _marshal is None:
-        lib()
-    return _marshal.pointer(t, name, dtype, shape)
+    return (_marshal or _checks()).pointer(t, name, dtype, shape)
 
 
 def moe_add_rmsnorm(x, residual, gamma, eps, s, y, q, q_scale, rstd, ws):
@@ -359,9 +366,7 @@ def moe_adamw_step(params, grads, masters, m, v, m_scale, v_scale, weight_decay,
     value per 256 elements) float8_e4m3fn m and float8_e5m2 v.  ``weight_decay``: a number, or one per tensor.  ``lr``
     (fp32[1]), ``step`` (int32[1], this step's number) and ``grad_scale`` (fp32[1] or None) are on the device."""
     n = len(params)
-    if _marshal is None:
-        lib()
-    p, g, masters, m, v, m_scale, v_scale, sizes, codes = _marshal.optimizer(params, grads, masters, m, v, m_scale, v_scale)
+    p, g, masters, m, v, m_scale, v_scale, sizes, codes = (_marshal or _checks()).optimizer(params, grads, masters, m, v, m_scale, v_scale)
     if not isinstance(weight_decay, (list, tuple)):
         weight_decay = [weight_decay] * n
     elif len(weight_decay) != n:
