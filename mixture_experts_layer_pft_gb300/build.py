@@ -3,7 +3,8 @@
 Each translation unit compiles in parallel into ``_build/``; the objects are linked into one
 shared library next to this file.  Nothing is rebuilt when every object is newer than its
 source and the headers.  ``csrc/marshal.cpp``, the binding's argument checks, becomes the Python
-module ``_marshal.so`` beside it (host code; torch's headers).
+module ``_marshal.so`` beside it (host code; torch's headers), and is built again for another
+Python or torch.
 """
 
 from __future__ import annotations
@@ -20,6 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_pft.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_KEY = os.path.join(BUILD, "marshal.txt")  # the Python and torch that MARSHAL was built for
 
 SOURCES = ["api.cu", "gather.cu", "route.cu", "pft.cu", "pft_noalloc.cu", "gemm_simt.cu", "gemm_tc.cu", "router_tc.cu", "gshard.cu", "gemm_f32tc.cu",
            "norm.cu", "adamw.cu", "w4.cu"]
@@ -44,6 +46,19 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _marshal_key() -> str:
+    import torch
+
+    return f"python {sys.version}\ntorch {torch.__version__} {os.path.dirname(torch.__file__)}\n"
+
+
+def _marshal_stale(source: str) -> bool:
+    if _stale(MARSHAL, [source]) or not os.path.exists(MARSHAL_KEY):
+        return True
+    with open(MARSHAL_KEY) as f:
+        return f.read() != _marshal_key()
 
 
 def _marshal_command(source: str) -> list:
@@ -75,7 +90,8 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
             jobs.append([nvcc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o])
 
     source = os.path.join(CSRC, "marshal.cpp")
-    if force or _stale(MARSHAL, [source]):
+    marshal = force or _marshal_stale(source)
+    if marshal:
         jobs.insert(0, _marshal_command(source))
 
     def run(cmd):
@@ -90,6 +106,9 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         list(ex.map(run, jobs))
+    if marshal:
+        with open(MARSHAL_KEY, "w") as f:
+            f.write(_marshal_key())
     if force or _stale(LIB, objs):
         run([nvcc, *ARCH, "-shared", "-o", LIB, *objs])
     return LIB

@@ -36,3 +36,35 @@ else:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def commands(build, monkeypatch):
+    """What build() would run, without running it."""
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    build.build()
+    return ran
+
+
+def test_it_is_built_again_for_another_torch_or_python(built, monkeypatch):
+    import torch
+
+    key = built.MARSHAL_KEY
+    monkeypatch.setattr(built, "MARSHAL_KEY", key + ".test")  # what is written here is not the tree's
+    try:
+        commands(built, monkeypatch)
+        assert commands(built, monkeypatch) == []  # built for this torch and this Python
+        monkeypatch.setattr(torch, "__version__", "0.0.1")
+        ran = commands(built, monkeypatch)
+        assert len(ran) == 1 and any(a.endswith("marshal.cpp") for a in ran[0])
+        assert commands(built, monkeypatch) == []
+        monkeypatch.setattr(sys, "version", "another")
+        assert len(commands(built, monkeypatch)) == 1
+    finally:
+        if os.path.exists(key + ".test"):
+            os.remove(key + ".test")
