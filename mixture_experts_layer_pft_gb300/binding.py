@@ -122,9 +122,16 @@ def _p(t):
     return t.data_ptr()
 
 
+# The current stream's handle alone: building torch's Stream object costs more than the rest of a call's marshalling.  These two
+# are not of torch's public interface; without them the public one is asked.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream():
-    # the handle alone: building torch's Stream object costs more than the rest of a call's marshalling
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if _raw_stream is None or _raw_device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_raw_device())
 
 
 def _call(name, *args):
