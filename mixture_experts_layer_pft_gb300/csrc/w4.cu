@@ -1013,9 +1013,9 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ 
   for (int i = threadIdx.x; i < half * 64; i += 256) {
     const int n = i / half, b = i % half;
     if (n0 + n >= N) continue;
-    const float s = fmaxf(sc[n], 1e-30f);
+    const float s = sc[n];
     auto code = [&](float w) {
-      const float z = rintf(w / s);
+      const float z = s == 0.f ? 0.f : rintf(w / s);
       return isnan(z) ? 8 : (int)fminf(fmaxf(z, -8.f), 7.f) + 8;
     };
     const int lo = code(tile[2 * b][n]), hi = code(tile[2 * b + 1][n]);

@@ -116,7 +116,7 @@ def quantize_w4(W, group):
     w = np.pad(np.asarray(W, np.float32).transpose(0, 2, 1), ((0, 0), (0, 0), (0, n * group - K))).reshape(E, N, n, group)
     s = np.abs(w).max(3) / _f32(7.0)
     s = torch.from_numpy(s).to(torch.bfloat16).float().numpy()
-    c = np.clip(np.rint(w / np.maximum(s, _f32(1e-30))[..., None]), -8, 7).astype(np.int32) + 8
+    c = np.clip(np.rint(w / np.where(s == 0, _f32(1), s)[..., None]), -8, 7).astype(np.int32) + 8
     c = c.reshape(E, N, n * group)[:, :, :K].astype(np.uint8)
     return c[:, :, 0::2] | (c[:, :, 1::2] << 4), s
 
