@@ -416,8 +416,9 @@ int moe_add_rmsnorm_bwd(const void* dy, const void* s, const float* gamma, const
  * seeds and steps give equal states.  All-zero codes and scales are the state before the first step.
  * lr: fp32[1], step: int32[1] (>= 1, the number of this step), grad_scale: fp32[1] or NULL (1), on the
  * device, so that a captured step follows them.  step < 1 sets MOE_STATUS_BAD_INDEX and changes nothing.
- * In the root, v / (1 - beta2^t) counts as 2^-126 at least.  An element whose g^2 is not finite keeps p, m and v (in 8 bits as they stand for; a new block scale
- * may round them again) and sets MOE_STATUS_NOT_FINITE.  0 <= beta1, beta2 < 1; eps > 0.
+ * In the root, v / (1 - beta2^t) counts as 2^-126 at least; root and quotient are each within 2 units of their last place.  An
+ * element whose g^2 is not finite keeps p, m and v (in 8 bits as they stand for; a new block scale may round them again) and
+ * sets MOE_STATUS_NOT_FINITE.  0 <= beta1, beta2 < 1; eps > 0.
  */
 int moe_adamw_step(int n, void* const* params, const void* const* grads, float* const* masters, void* const* ms,
                    void* const* vs, float* const* m_scales, float* const* v_scales, const int64_t* numels,
@@ -444,11 +445,14 @@ int moe_quantize_w4(const void* W, int E, int K, int N, int dtype, int group, vo
  * fp32, as moe_add_rmsnorm writes them; x_scale is NULL otherwise.  topk_idx: [T,k] int32, topk_w:
  * [T,k] fp32 (these three at any address of their type: rows of a larger batch may be passed as they are).
  * W1q, W3q: [E,f,h/2], W1s, W3s: [E,f,ceil(h/group)]; W2q: [E,h,f/2], W2s: [E,h,ceil(f/group)].  y: [T,h] dtype.
- * Sums are fp32 over the exact 4-bit values, a group's sum is scaled once.  One token (k <= 64), and up to 8 tokens with
- * T*k <= 12, that fit in shared memory: x and a are rounded to 24 bits of the largest of 16 neighbours (to zeros where that is below 2^-90), and y sums the experts in ascending order instead of j's, whatever else is in the batch.
- * Otherwise x is read as it is (MOE_BF16, MOE_E4M3) or keeps 23 significant bits (MOE_F32), a keeps 11 (MOE_BF16) or 23, of both
- * what is below 2^-34 of the largest of 128 neighbours is lost (all where that is below 2^-90; nothing of e4m3), and the order of the fp32 sums may go by the batch's routing (deterministically).  An id outside
- * [0,E) sets MOE_STATUS_BAD_INDEX and adds nothing.  A token with a value that is not a finite number gets NaN or
+ * Sums are fp32 over the exact 4-bit values, a group's sum is scaled once.
+ * One token (k <= 64), and up to 8 tokens with T*k <= 12, that fit in shared memory: x and a are rounded to 24 bits of the
+ * largest of 16 neighbours (to zeros where that is below 2^-90), and y sums the experts in ascending order instead of j's,
+ * whatever else is in the batch.
+ * Otherwise x is read as it is (MOE_BF16, MOE_E4M3) or keeps 23 significant bits (MOE_F32), and a keeps 11 (MOE_BF16) or 23; of
+ * both, what is below 2^-34 of the largest of 128 neighbours is lost, and all where that is below 2^-90 (nothing of e4m3).  The
+ * order of the fp32 sums goes by topk_idx alone: equal calls give equal bits.
+ * An id outside [0,E) sets MOE_STATUS_BAD_INDEX and adds nothing.  A token with a value that is not a finite number gets NaN or
  * infinities, and no other token does.
  * Requires h % 32 == 0, f % 32 == 0, h*f < 2^32, 1 <= k <= E <= 1024 and T*k <= 65536.
  */

@@ -324,8 +324,8 @@ __device__ __forceinline__ Factors factors(const AdamwArgs<N>& a, int step, int 
 
 // A warp's `blocks` blocks.  With 32-bit states HBM is the bound and few warps an SM reach it when each loads a block
 // ahead.  8-bit states are bound by some 80 instructions an element, which want warps to choose from: 40 an SM without a
-// block ahead take 1454 us for the Small layer, 32 take 1497, 48 (spilling) 1529, 32 with a block ahead in registers
-// (spilling) 1581, 24 with two or three ahead in shared memory 1702.
+// block ahead take 1454 us for the Small layer, 32 take 1497, 48 1529, 32 with a block ahead in registers 1581, 24 with two
+// or three ahead in shared memory 1702.  (40 have 48 registers each and spill 176 bytes a thread; 48 spill more.)
 template <bool BF16, bool Q8, int N>
 __device__ __forceinline__ void run_warp(const AdamwArgs<N>& a, const AdamwTensor& q, int tensor, int step, long long base,
                                          int blocks, int lane) {

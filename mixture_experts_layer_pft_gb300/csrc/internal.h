@@ -128,8 +128,10 @@ struct AdamwScalars {
 constexpr int kAdamwMaxTensors = 384;  // of one launch
 void launch_adamw(const AdamwTensor* t, int n, int first_tensor, const AdamwScalars& c, cudaStream_t st);
 
-// w4.cu -- routed experts over 4-bit weights.  Scratch: a's bf16 planes ([2 or 3][T*k, f]), the experts' output rows
-// ([T*k, h] fp32), x's planes ([1 or 3][T, h]) and the rows by expert; w4_scratch: its bytes, and the parts' offsets.
+// w4.cu -- routed experts over 4-bit weights.  Scratch: `a` ([T*k, f] in fp32; for few tokens as three bytes and a scale for
+// 16), the experts' output rows ([T*k, h] fp32), f16 planes of x ([T, h]) and of `a`, one in 16-bit layers and two in fp32
+// ones, each with an fp32 scale for 128 values, and the plan of units with the rows by expert; w4_scratch: its bytes, and the
+// parts' offsets.
 struct W4Scratch {
   size_t a, rows, x_planes, a_planes, plan;
 };

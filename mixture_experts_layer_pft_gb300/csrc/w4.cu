@@ -3,15 +3,17 @@
 //   W[n, i] = (nibble - 8) * scale[n, i / G];  a = silu(W1_e x) * (W3_e x);  y[t] = sum_j w_j W2_e a.
 //
 // The floor is the active experts' bytes: 182 MB, 27 us, for one token of the Large layer (h 7168, f 2048, k 8 of 256).  What
-// bounds the kernels instead is instructions: a byte of weights is two products, and turning nibbles into operands costs
-// more than multiplying them.  Measured on this GPU, instructions a clock and SM: dp4a, LOP3, IMAD, I2F and bf16x2 FMA 1.9
+// bounds the kernels instead is instructions and their latency: a byte of weights is two products, and turning nibbles into
+// operands costs more than multiplying them.  Measured on this GPU, instructions a clock and SM: dp4a, LOP3, IMAD, I2F and bf16x2 FMA 1.9
 // each, mma.sync bf16 16x8x16 0.50, mma.sync s8 16x8x32 0.06.  Two forms follow from that.
 //
 // "Few" (one token, or up to 8 and 12 rows, whose activations fit in shared memory): integers through dp4a, see below.
 // Two launches: the first writes `a`, the second adds each token's outputs over its experts in registers; it starts early and has its
 // first weights under way while the first still runs.  Large layer, one token in 8 bits: 52 us (51% of the floor's rate;
-// tensor cores in this place 86 us).  Small layer (h 2048, f 1408, 6 of 64): 14 us, of which the launches, the chain from
-// topk_idx to y and the host are most.
+// tensor cores in this place 86 us).  Of a warp's 330 and 238 instructions a step of 16 outputs x 128 inputs (two matrices, one),
+// some 208 and 112 are the products and their reads of shared memory; the rest converts x in every block, finds experts and
+// addresses and copies.  2.4 are issued a clock and SM, and half of a warp's wait in the first kernel is for its next weights.
+// Small layer (h 2048, f 1408, 6 of 64): 14 us, of which the launches, the chain from topk_idx to y and the host are most.
 //
 // "Many": tensor cores with 16 outputs as M and token rows as N.  A nibble n masked into the mantissa of an f16 1024 is
 // 1024 + n, and n - 8 after a subtraction, exactly: eight nibbles are operands after nine instructions (in bf16 eleven).
@@ -19,7 +21,7 @@
 // exactly; x in fp32 as two, of 23 bits; `a` as one of 11 bits beside y's 8 in 16-bit layers, as two in fp32 ones (bf16
 // planes take one more each).  Groups' sums are kept apart in fp32 and scaled once, so no weight is rounded.  An expert's
 // rows come in units of 16 (fp32: 8); experts' output rows go to scratch, and a combine adds them.  64 tokens of the Medium
-// layer (h 5120, f 1536, 6 of 128, skewed): 171 to 183 us against a floor of 36 (with bf16 operands 213); 13 fp32 tokens of
+// layer (h 5120, f 1536, 6 of 128, skewed): 175 to 195 us against a floor of 36 (with bf16 operands 213); 13 fp32 tokens of
 // the long-sequence layer (h f 2048, 2 of 128, groups of 32): 53 against 5 (70).  Unpacking for one or two tiles of rows,
 // copies and the groups' scales, some 12 instructions a product at 2 a clock, as two blocks an SM do not cover their
 // latencies, and five launches are the rest.
@@ -1068,8 +1070,10 @@ void few(const W4Ffn& p, cudaStream_t st) {
   count_launch(st);
   const FewArgs down{nullptr, nullptr, p.topk_idx, p.topk_w, p.T, p.k, p.E, p.f, p.h,
                      {{static_cast<const unsigned char*>(p.W2q), static_cast<const __nv_bfloat16*>(p.W2s)}, {}}, bytes, scales, p.y, p.status};
-  // One token's second kernel with three blocks an SM spills some of its registers, which a grid of more than two an SM is
-  // glad to pay (Large layer: 46 us for both kernels, 51 with two) and a smaller one is not (Small layer: 17 and 14 us).
+  // One token's second kernel has 80 registers with three blocks an SM, and up to 120 with two.  A grid of more than two an SM
+  // takes three rather than a second round (Large layer: 52 us for both kernels, with two 56; Medium: 30.5 and 32.3).  A smaller
+  // one runs at once either way, and keeps more of its loads under way with two (Small layer: 13.9 us, with three 14.4; in
+  // groups of 32, where three spill, 23.6 and 25.6; h 4096, f 1408, 6 experts: 21.7 and 24.0).
   const size_t shared = few_bytes(p.T * p.k, p.f);
   const int blocks = p.h / kTile;
   if (ROWS == 1 && blocks > 2 * num_sms()) {
