@@ -79,8 +79,12 @@ class AdamW:
     def step(self, grad_scale: torch.Tensor | None = None):
         """One step on the current stream; ``grad_scale`` (fp32[1] on the device) multiplies every gradient."""
         self.step_count.add_(1)
-        B.moe_adamw_step(self.params, self.grads, self.masters, self.m, self.v, self.m_scale, self.v_scale, self.weight_decay,
-                         self.lr, self.step_count, grad_scale, *self.betas, self.eps, self.seed, self.ws)
+        try:
+            B.moe_adamw_step(self.params, self.grads, self.masters, self.m, self.v, self.m_scale, self.v_scale, self.weight_decay,
+                             self.lr, self.step_count, grad_scale, *self.betas, self.eps, self.seed, self.ws)
+        except (TypeError, ValueError, B.MoEError):  # refused: no step was made
+            self.step_count.sub_(1)
+            raise
 
 
 class DecodeBlock:
